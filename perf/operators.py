@@ -20,7 +20,7 @@ import torch
 own = False
 
 QMAX = {"int8": 127.0, "e4m3": 448.0}
-E_MIN, E_MAX = -120, 121  # exponents of the scales
+E_MIN, E_MAX = -120, 122  # exponents of the scales
 
 
 def _dt(name):
