@@ -20,7 +20,8 @@ __all__ = [
     "pack_in_major", "col_norms", "select_topk", "stat_topk_threshold", "sparse_matvec",
     "sparse_ffn_swiglu", "ffn_ws_view", "ffn_prepare", "declared_symbols", "sparse_matvec_noalloc",
     "dense_matvec", "dense_ffn_swiglu", "spark_ffn", "ds_channel_absmean", "ds_calibrate_channels",
-    "ds_label_build", "ds_decode_attention",
+    "ds_label_build", "ds_decode_attention", "Kv8Cache", "kv8_cache", "kv8_plan", "kv8_write", "kv8_read",
+    "kv8_attention",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libwina.so")
@@ -32,6 +33,8 @@ F32, BF16 = 0, 1
 LAYOUT_OUT_IN, LAYOUT_IN_MAJOR = 0, 1
 GATE_TOPK, GATE_STAT, GATE_DENSE = 0, 1, 2
 OP_SELECT_TOPK, OP_STAT_THRESHOLD, OP_SPARSE_MATVEC, OP_FFN_SWIGLU, OP_SPARK_FFN, OP_DENSE_FFN = 0, 1, 2, 3, 4, 5
+OP_KV8_ATTENTION = 6
+KV8_INT8, KV8_E4M3 = 0, 1
 
 
 class WinaError(RuntimeError):
@@ -51,6 +54,12 @@ class _FfnT(ctypes.Structure):
 class _FfnView(ctypes.Structure):
     _fields_ = [("h", ctypes.c_size_t), ("keep_gate", ctypes.c_size_t), ("keep_up", ctypes.c_size_t),
                 ("keep_down", ctypes.c_size_t), ("stamps", ctypes.c_size_t), ("cta_t", ctypes.c_size_t)]
+
+
+class _Kv8T(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("format", ctypes.c_int), ("n_pages", ctypes.c_int64),
+                ("heads", ctypes.c_int64), ("page", ctypes.c_int64), ("dh", ctypes.c_int64)]
 
 
 def _load() -> ctypes.CDLL:
@@ -81,6 +90,11 @@ def _load() -> ctypes.CDLL:
         "ds_decode_smem_bytes": (SZ, [I64, I64, I64]),
         "ds_decode_attention": (E, [P, E, P, P, P, E, P, I64, I64, I64, I64, I64, I64, P, I64, ctypes.c_float, P, P, P,
                                     P]),
+        "kv8_plan": (E, [P, P, I64, I64, P, I64, P, I64, P, I64, P, P, P, P, P, P, P]),
+        "kv8_write": (E, [ctypes.POINTER(_Kv8T), P, P, E, I64, I64, I64, P, P, P]),
+        "kv8_read": (E, [ctypes.POINTER(_Kv8T), P, I64, P, P, E, P, P]),
+        "kv8_attention": (E, [ctypes.POINTER(_Kv8T), P, E, I64, I64, I64, P, I64, P, P, I64, I64, ctypes.c_float, I64,
+                              ctypes.c_float, P, P, SZ, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -472,3 +486,211 @@ def ds_decode_attention(q, K, V, label, channels, seq_len, k: int, scale: float 
                                    _ptr(idx) if idx is not None else None, _ptr(sc) if sc is not None else None,
                                    _ptr(status) if status is not None else None, _stream()), "ds_decode_attention")
     return out, idx, sc
+
+
+# ------------------------------------------------------------------------------------
+# the 8-bit paged key/value cache
+# ------------------------------------------------------------------------------------
+
+
+def _on(dev, **named):
+    """Every tensor given is on `dev`, of the dtype named (None: any) and contiguous."""
+    for name, (t, dtype) in named.items():
+        if t is None:
+            continue
+        if t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, not on {t.device}")
+        if dtype is not None and t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _launch(dev, where, fn, *args):
+    """Call `fn` with the current stream of `dev` as its last argument, `dev` being current."""
+    torch = _torch()
+    if dev.type != "cuda":
+        raise ValueError(f"{where}: tensors must be on a CUDA device")
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if dev.index == torch.cuda.current_device():
+        code = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, stream)
+    _check(code, where)
+
+
+@dataclass
+class Kv8Cache:
+    """The pages of an 8-bit key/value cache: k, v int8 or float8_e4m3fn
+    [n_pages][heads][page][dh], and one float32 scale per page and head, k_scale and v_scale
+    [n_pages][heads]; a value is scale * byte."""
+    k: object
+    v: object
+    k_scale: object
+    v_scale: object
+
+    @property
+    def n_pages(self) -> int:
+        return int(self.k.shape[0])
+
+    @property
+    def heads(self) -> int:
+        return int(self.k.shape[1])
+
+    @property
+    def page(self) -> int:
+        return int(self.k.shape[2])
+
+    @property
+    def dh(self) -> int:
+        return int(self.k.shape[3])
+
+    def _struct(self) -> _Kv8T:
+        torch = _torch()
+        k, v = self.k, self.v
+        fmt = {torch.int8: KV8_INT8, torch.float8_e4m3fn: KV8_E4M3}.get(k.dtype)
+        if fmt is None or v.dtype != k.dtype:
+            raise TypeError("k and v must both be int8 or both float8_e4m3fn")
+        if k.dim() != 4 or v.shape != k.shape:
+            raise ValueError("k and v must be [n_pages][heads][page][dh], of one shape")
+        _on(k.device, k=(k, None), v=(v, None), k_scale=(self.k_scale, torch.float32),
+            v_scale=(self.v_scale, torch.float32))
+        n, h, page, dh = k.shape
+        if self.k_scale.shape != (n, h) or self.v_scale.shape != (n, h):
+            raise ValueError("k_scale and v_scale must be [n_pages][heads]")
+        return _Kv8T(k.data_ptr(), v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(), fmt, n, h, page, dh)
+
+
+def kv8_cache(n_pages: int, heads: int, page: int, dh: int, dtype=None, device=None) -> Kv8Cache:
+    """A zero-filled 8-bit cache (dtype: int8, the default, or float8_e4m3fn)."""
+    torch = _torch()
+    dtype = torch.int8 if dtype is None else dtype
+    if dtype not in (torch.int8, torch.float8_e4m3fn):
+        raise TypeError("dtype must be int8 or float8_e4m3fn")
+    dev = device or "cuda"
+    k, v = (torch.zeros((n_pages, heads, page, dh), dtype=torch.int8, device=dev).view(dtype) for _ in range(2))
+    ks, vs = (torch.zeros((n_pages, heads), dtype=torch.float32, device=dev) for _ in range(2))
+    return Kv8Cache(k, v, ks, vs)
+
+
+def kv8_plan(seq_len, new_len, table, free_pages, n_free, page: int, tokens: int, kv_len=None, cu_q=None, slots=None,
+             positions=None, n_free_out=None, status=None):
+    """Where one step's tokens go. seq_len, new_len int32 [B] (new_len < 0 ends a request);
+    table int32 [B][width], free_pages int32 [cells] and its count n_free int32 [1] are the
+    page tables and the stack of free pages, updated in place (the count into n_free_out).
+    Returns (kv_len [B], cu_q [B + 1], slots [tokens], positions [tokens], n_free_out [1]),
+    allocated where not given; kv_len may be seq_len itself and n_free_out n_free."""
+    torch = _torch()
+    i32, dev = torch.int32, seq_len.device
+    B = seq_len.shape[0]
+    new = lambda n: torch.empty(n, dtype=i32, device=dev)  # noqa: E731
+    kv_len = new(B) if kv_len is None else kv_len
+    cu_q = new(B + 1) if cu_q is None else cu_q
+    slots = new(tokens) if slots is None else slots
+    positions = new(tokens) if positions is None else positions
+    n_free_out = new(1) if n_free_out is None else n_free_out
+    _on(dev, seq_len=(seq_len, i32), new_len=(new_len, i32), table=(table, i32), free_pages=(free_pages, i32),
+        n_free=(n_free, i32), kv_len=(kv_len, i32), cu_q=(cu_q, i32), slots=(slots, i32), positions=(positions, i32),
+        n_free_out=(n_free_out, i32), status=(status, i32))
+    if seq_len.dim() != 1 or new_len.shape != seq_len.shape or table.dim() != 2 or table.shape[0] != B:
+        raise ValueError("seq_len and new_len must be [B] and table [B][width]")
+    if kv_len.numel() != B or cu_q.numel() != B + 1 or slots.numel() != tokens or positions.numel() != tokens or \
+            n_free.numel() != 1 or n_free_out.numel() != 1:
+        raise ValueError("kv_len [B], cu_q [B + 1], slots and positions [tokens], n_free and n_free_out [1]")
+    _launch(dev, "kv8_plan", lib.kv8_plan, _addr(seq_len), _addr(new_len), B, page, _addr(table), table.shape[1],
+            _addr(free_pages), free_pages.numel(), _addr(n_free), tokens, _addr(kv_len), _addr(cu_q), _addr(slots),
+            _addr(positions), _addr(n_free_out), _addr(status))
+    return kv_len, cu_q, slots, positions, n_free_out
+
+
+def _rows(t, name, heads, dh):
+    """The row stride of t [T][heads][dh], whose rows are contiguous and may lie apart."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dh:
+        raise ValueError(f"{name} must be [T][{heads}][{dh}]")
+    s = t.stride()
+    if s[2] != 1 or (heads > 1 and s[1] != dh):
+        raise ValueError(f"{name}'s rows must be contiguous (a token's heads side by side)")
+    return s[0] if t.shape[0] > 1 else heads * dh
+
+
+def kv8_write(cache: Kv8Cache, k, v, slots, status=None) -> Kv8Cache:
+    """New keys and values [T][heads][dh] (bf16 or float32, rows may be slices of a wider
+    tensor's) into the pages of `cache`, at slots int32 [T] (negative: skipped)."""
+    torch = _torch()
+    c = cache._struct()
+    dev = cache.k.device
+    dt = _dt(k)
+    if v.dtype != k.dtype:
+        raise TypeError("k and v must have one dtype")
+    if k.device != dev or v.device != dev:
+        raise ValueError(f"k and v must be on {dev}")
+    ld_k, ld_v = _rows(k, "k", c.heads, c.dh), _rows(v, "v", c.heads, c.dh)
+    _on(dev, slots=(slots, torch.int32), status=(status, torch.int32))
+    T = k.shape[0]
+    if v.shape[0] != T or slots.numel() != T:
+        raise ValueError("k, v and slots must have one length")
+    _launch(dev, "kv8_write", lib.kv8_write, ctypes.byref(c), _addr(k), _addr(v), dt, T, ld_k, ld_v, _addr(slots),
+            _addr(status))
+    return cache
+
+
+def kv8_read(cache: Kv8Cache, slots, dtype=None, k=None, v=None, status=None):
+    """The cached rows at slots int32 [T] as (k, v) [T][heads][dh] of dtype (bf16, the
+    default, or float32; that of k and v where they are given); zeros for negative slots."""
+    torch = _torch()
+    c = cache._struct()
+    dev, T = cache.k.device, slots.numel()
+    shape = (T, c.heads, c.dh)
+    if k is None:
+        k = torch.empty(shape, dtype=dtype or (torch.bfloat16 if v is None else v.dtype), device=dev)
+    if v is None:
+        v = torch.empty(shape, dtype=k.dtype, device=dev)
+    dt = _dt(k)
+    if dtype is not None and k.dtype != dtype:
+        raise TypeError(f"k must be {dtype}")
+    _on(dev, slots=(slots, torch.int32), k=(k, None), v=(v, k.dtype), status=(status, torch.int32))
+    if tuple(k.shape) != shape or tuple(v.shape) != shape:
+        raise ValueError(f"k and v must be {list(shape)}")
+    _launch(dev, "kv8_read", lib.kv8_read, ctypes.byref(c), _addr(slots), T, _addr(k), _addr(v), dt, _addr(status))
+    return k, v
+
+
+def kv8_attention(cache: Kv8Cache, q, table, kv_len, cu_q=None, max_q: int = 1, scale: float = 0.0, window: int = 0,
+                  softcap: float = 0.0, ws: Workspace | None = None, out=None, status=None):
+    """Causal attention of q [T][Hq][dh] (bf16 or float32; rows may be slices of a wider
+    tensor's) over the pages: request b's queries are rows cu_q[b] .. cu_q[b + 1] - 1 (at
+    most max_q; cu_q None: one row each), the last of them at key kv_len[b] - 1. Returns out
+    [T][Hq][dh] in q's dtype; with `out` given, rows behind the last request stay as they were."""
+    torch = _torch()
+    c = cache._struct()
+    dev, i32 = cache.k.device, torch.int32
+    dt = _dt(q)
+    if q.device != dev:
+        raise ValueError(f"q must be on {dev}")
+    if q.dim() != 3:
+        raise ValueError("q must be [T][Hq][dh]")
+    T, Hq = q.shape[0], q.shape[1]
+    ld_q = _rows(q, "q", Hq, c.dh)
+    B = kv_len.numel()
+    if out is None:
+        out = torch.zeros((T, Hq, c.dh), dtype=q.dtype, device=dev)
+    _on(dev, table=(table, i32), kv_len=(kv_len, i32), cu_q=(cu_q, i32), out=(out, q.dtype), status=(status, i32))
+    if table.dim() != 2 or table.shape[0] != B or (cu_q is not None and cu_q.numel() != B + 1):
+        raise ValueError("table must be [B][width], kv_len [B] and cu_q [B + 1]")
+    if tuple(out.shape) != (T, Hq, c.dh):
+        raise ValueError(f"out must be {[T, Hq, c.dh]}")
+    if Hq < 1 or Hq % c.heads:
+        raise ValueError(f"{Hq} query heads over {c.heads} key/value heads")
+    if ws is None:
+        ws = Workspace(OP_KV8_ATTENTION, c.dh, max_q * (Hq // c.heads), 0, B, device=dev)
+    elif ws.buf.device != dev:
+        raise ValueError(f"ws must be on {dev}")
+    _launch(dev, "kv8_attention", lib.kv8_attention, ctypes.byref(c), _addr(q), dt, T, ld_q, Hq, _addr(table),
+            table.shape[1], _addr(kv_len), _addr(cu_q), B, max_q, scale, window, softcap, _addr(out), ws.buf.data_ptr(),
+            ws.nbytes, _addr(status))
+    return out

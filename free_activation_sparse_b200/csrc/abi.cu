@@ -207,6 +207,7 @@ extern "C" size_t wina_workspace_size(wina_op_t op, int64_t n, int64_t m, int64_
     case WINA_OP_FFN_SWIGLU: return ffn_ws_layout(n, m, batch).total;
     case WINA_OP_SPARK_FFN: return batch == 1 ? spark_ws_size(n, m) : 0;
     case WINA_OP_DENSE_FFN: return batch == 1 ? dense_ws_size(n, m) : 0;
+    case WINA_OP_KV8_ATTENTION: return kv8_attention_ws_size(n, m);
     default: return 0;
   }
 }

@@ -211,6 +211,11 @@ wina_status_t launch_silu_mul(const float* g, const float* u, float* h, int64_t 
 // Workspace bytes of spark_ffn_swiglu (spark.cu).
 size_t spark_ws_size(int64_t d, int64_t ffn);
 size_t dense_ws_size(int64_t d, int64_t ffn);
+// Workspace bytes of kv8_attention (kv8_attn.cu): head width, query rows of a request per
+// key/value head.
+size_t kv8_attention_ws_size(int64_t dh, int64_t rows);
+// The limits of an 8-bit cache descriptor (kv8.cu): WINA_OK or WINA_ERR_INVALID_ARG.
+wina_status_t kv8_cache_check(const kv8_cache_t* c);
 // The union path (union_gemm.cu); ws is the union region of the workspace. premarked: the
 // union flags were already set by the gate that made the lists (launch_select_topk's
 // uflag), which serves a single token block (batch <= kUBlock).

@@ -82,7 +82,8 @@ typedef enum {
   WINA_OP_SPARSE_MATVEC = 2,
   WINA_OP_FFN_SWIGLU = 3,
   WINA_OP_SPARK_FFN = 4,
-  WINA_OP_DENSE_FFN = 5
+  WINA_OP_DENSE_FFN = 5,
+  WINA_OP_KV8_ATTENTION = 6
 } wina_op_t;
 
 /* The three projections of a SwiGLU FFN, already packed input-major:
@@ -159,6 +160,8 @@ double wina_normal_quantile(double p);
  *   WINA_OP_FFN_SWIGLU:    n = d, m = ffn, k ignored, batch = tokens.
  *   WINA_OP_SPARK_FFN:     n = d, m = ffn, k ignored, batch = 1.
  *   WINA_OP_DENSE_FFN:     n = d, m = ffn, k ignored, batch = 1.
+ *   WINA_OP_KV8_ATTENTION: n = dh, m = max_q * Hq / Hkv (a request's query rows per
+ *                          key/value head, at most), k ignored, batch = requests.
  *   WINA_OP_SELECT_TOPK, WINA_OP_STAT_THRESHOLD: 0.                                  */
 size_t wina_workspace_size(wina_op_t op, int64_t n, int64_t m, int64_t k, int64_t batch);
 
@@ -409,6 +412,118 @@ wina_status_t ds_decode_attention(const void* q, wina_dtype_t qdt, const void* K
                                   int64_t Tmax, int64_t dh, int64_t r, const int32_t* seq_len, int64_t k,
                                   float scale, float* out, int32_t* idx_out, float* scores_out,
                                   int32_t* status_dev, wina_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
+ * The 8-bit paged key/value cache: pages of `page` tokens, held as int8 or e4m3 with one
+ * float32 scale for each page and key/value head, so that a value is scale * byte.
+ *   k, v:             device [n_pages][heads][page][dh] bytes (read and written)
+ *   k_scale, v_scale: device float32 [n_pages][heads]
+ * A page and head is one contiguous run of page * dh bytes. Token t of a request is at
+ * place t % page of page table[request][t / page]; its slot is page_index * page + place.
+ * The four calls of a decode step: kv8_plan (where the step's tokens go), kv8_write (their
+ * keys and values into the pages), kv8_attention (their queries over the pages), and
+ * kv8_read where cached rows are wanted back (for example as the input of
+ * ds_channel_absmean and ds_label_build). The index arrays stay on the device, so a step
+ * can be captured in a graph and replayed with other lengths.
+ *   page in {16, 32, 64, 128}; dh in {64, 128, 256}; n_pages * page < 2^31; heads <= 1024.
+ * A page index outside [0, n_pages) is never followed: its tokens are left out and
+ * WINA_ERR_INVALID_ARG is recorded in status_dev.
+ * --------------------------------------------------------------------------------- */
+
+typedef enum { KV8_INT8 = 0, KV8_E4M3 = 1 } kv8_format_t;
+
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  kv8_format_t format;
+  int64_t n_pages;
+  int64_t heads;
+  int64_t page;
+  int64_t dh;
+} kv8_cache_t;
+
+/* One step's places, from the requests' lengths, in one launch. Request b has seq_len[b]
+ * cached tokens and brings new_len[b] more (0 or more); new_len[b] < 0 ends it: its
+ * ceil(seq_len / page) pages go back and its length becomes 0.
+ *   free_pages: device int32 [cells], a stack of free page indices of which the lowest
+ *     *n_free cells are in use. The ended requests' pages are pushed first, in the order of
+ *     requests and of their pages; then the others pop the pages they lack, in the order of
+ *     requests, each from the top down. Popped cells keep what they held.
+ *   table: device int32 [B][width]: the popped pages are written behind a request's present
+ *     ones; all else is left as it was.
+ *   kv_len: device int32 [B]: the lengths with the new tokens (may be seq_len itself).
+ *   cu_q: device int32 [B + 1]: exclusive prefix sums of the new tokens (at most `tokens`).
+ *   slots: device int32 [tokens]: every new token's slot, in the order of requests; -1 for
+ *     the places behind the last token (a padded batch) and for tokens without a page.
+ *   positions: optional device int32 [tokens]: every new token's position in its request
+ *     (0 where slots is -1).
+ *   n_free_out: device int32 [1]: the pages free afterwards (may be n_free itself).
+ * Where the pages, or the `tokens` places, do not suffice, the requests up to the first
+ * that lacks them are served and the others are not: they take no page, their slots are -1
+ * and their kv_len stays seq_len, and WINA_ERR_CAPACITY is recorded. A request with
+ * seq_len < 0 or more tokens than width * page is left out the same way (kv_len: seq_len
+ * clamped to the table) with WINA_ERR_INVALID_ARG, as is an *n_free outside [0, cells]
+ * (clamped). Pages pushed past the last cell are lost, with WINA_ERR_CAPACITY.
+ * The outputs other than the stack's cells depend on the inputs alone, so with separate
+ * kv_len and n_free_out the call can be repeated.
+ *   1 <= B <= 8192; tokens >= 0; width >= 1, width * page < 2^31; cells >= 1. */
+wina_status_t kv8_plan(const int32_t* seq_len, const int32_t* new_len, int64_t B, int64_t page, int32_t* table,
+                       int64_t width, int32_t* free_pages, int64_t cells, const int32_t* n_free, int64_t tokens,
+                       int32_t* kv_len, int32_t* cu_q, int32_t* slots, int32_t* positions, int32_t* n_free_out,
+                       int32_t* status_dev, wina_stream_t stream);
+
+/* New keys and values into their pages. For each page and head that gets tokens:
+ *   amax = max |x| over the new rows;  s = the smallest power of two with amax <= qmax * s
+ *   (qmax 127 for int8, 448 for e4m3; exponents kept within [-120, 122]);
+ *   a page whose place 0 is written starts anew with that s; any other keeps the larger of
+ *   s and its present scale, and where that grows its older rows (the places before the
+ *   first new one) are rounded again to the new scale;
+ *   a byte is x / scale rounded to nearest even (exact up to that one rounding, since the
+ *   scales are powers of two).
+ * Where a new row holds an infinity or a NaN, the page and head's scale becomes NaN and the
+ * rows written are 0, so that attention over it gives NaN as it would with unquantised
+ * values, until the page starts anew.
+ *   k, v: device [T][heads][dh] of xdt with ld_k, ld_v elements from one token's row to
+ *     the next (slices of a fused projection's output); 16-byte aligned, ld * size a
+ *     multiple of 16 bytes, ld >= heads * dh.
+ *   slots: device int32 [T]: a negative slot's row is skipped. The rows that go to one page
+ *     are consecutive, at ascending places, as kv8_plan makes them; where two runs of rows
+ *     name one page, what that page holds afterwards is unspecified.
+ *   T >= 0 (0 launches nothing). */
+wina_status_t kv8_write(const kv8_cache_t* cache, const void* k, const void* v, wina_dtype_t xdt, int64_t T,
+                        int64_t ld_k, int64_t ld_v, const int32_t* slots, int32_t* status_dev, wina_stream_t stream);
+
+/* Cached rows back as numbers: k[t] and v[t] = scale * byte of slot slots[t] (float32, then
+ * rounded once to xdt); zeros for a negative slot or one outside the cache.
+ *   k, v: device [T][heads][dh] of xdt, contiguous (either may be NULL);  T >= 0. */
+wina_status_t kv8_read(const kv8_cache_t* cache, const int32_t* slots, int64_t T, void* k, void* v, wina_dtype_t xdt,
+                       int32_t* status_dev, wina_stream_t stream);
+
+/* Causal attention of a step's queries over the pages. Request b's queries are rows
+ * cu_q[b] .. cu_q[b + 1] - 1 (with cu_q NULL: one row each, T == B), its last query stands
+ * at its last key: query i of n is at position kv_len[b] - n + i and sees the keys at or
+ * before it, the last `window` of them where window > 0. Query head h reads key/value head
+ * h / (Hq / Hkv).
+ *   s_j = (q . k_j) * scale (scale <= 0: 1 / sqrt(dh)); with softcap > 0,
+ *   s_j = softcap * tanh(s_j / softcap);  out = sum_j softmax(s)_j v_j
+ * A query that sees no key gives zeros. Rows behind cu_q[B] are left as they were.
+ *   q: device [T][Hq][dh] of qdt, ld_q elements from row to row (16-byte aligned rows);
+ *   out: device [T][Hq][dh] of qdt, contiguous; products and softmax in float32 (see the
+ *     kernels for what is rounded on the way), one rounding to qdt at the end.
+ *   table: device int32 [B][width];  kv_len: device int32 [B].
+ *   max_q: the most queries of any request (a host bound; queries beyond it are left
+ *     unwritten and WINA_ERR_INVALID_ARG is recorded).
+ *   ws: device scratch of wina_workspace_size(WINA_OP_KV8_ATTENTION, dh, max_q * Hq / Hkv,
+ *     0, B) bytes (see that function).
+ *   A kv_len outside [0, width * page] or a cu_q that descends or leaves [0, T] is clamped
+ *   and recorded as WINA_ERR_INVALID_ARG. 1 <= B <= 8192, Hq / Hkv <= 64, T <= 2^24.
+ *   Deterministic: fixed-order sums throughout. */
+wina_status_t kv8_attention(const kv8_cache_t* cache, const void* q, wina_dtype_t qdt, int64_t T, int64_t ld_q,
+                            int64_t Hq, const int32_t* table, int64_t width, const int32_t* kv_len,
+                            const int32_t* cu_q, int64_t B, int64_t max_q, float scale, int64_t window, float softcap,
+                            void* out, void* ws, size_t ws_bytes, int32_t* status_dev, wina_stream_t stream);
 
 #ifdef __cplusplus
 }
