@@ -512,7 +512,7 @@ wina_status_t kv8_read(const kv8_cache_t* cache, const int32_t* slots, int64_t T
  *   q: device [T][Hq][dh] of qdt, ld_q elements from row to row (16-byte aligned rows);
  *   out: device [T][Hq][dh] of qdt, contiguous; products and softmax in float32 (see the
  *     kernels for what is rounded on the way), one rounding to qdt at the end.
- *   table: device int32 [B][width];  kv_len: device int32 [B].
+ *   table: device int32 [B][width], width * page <= 2^30;  kv_len: device int32 [B].
  *   max_q: the most queries of any request (a host bound; queries beyond it are left
  *     unwritten and WINA_ERR_INVALID_ARG is recorded).
  *   ws: device scratch of wina_workspace_size(WINA_OP_KV8_ATTENTION, dh, max_q * Hq / Hkv,
