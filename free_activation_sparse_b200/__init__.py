@@ -493,17 +493,15 @@ def ds_decode_attention(q, K, V, label, channels, seq_len, k: int, scale: float 
 # ------------------------------------------------------------------------------------
 
 
-def _on(dev, **named):
-    """Every tensor given is on `dev`, of the dtype named (None: any) and contiguous."""
-    for name, (t, dtype) in named.items():
-        if t is None:
-            continue
-        if t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, not on {t.device}")
-        if dtype is not None and t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+def _on(dev, names, *tensors):
+    """Every tensor given (named in `names`) is a contiguous int32 tensor on `dev`."""
+    i32 = _torch().int32
+    for i, t in enumerate(tensors):
+        if t is not None and not (t.dtype is i32 and t.device == dev and t.is_contiguous()):
+            name = names.split()[i]
+            if t.dtype is not i32:
+                raise TypeError(f"{name} must be int32, not {t.dtype}")
+            raise ValueError(f"{name} must be contiguous and on {dev} (is on {t.device})")
 
 
 def _addr(t):
@@ -512,16 +510,18 @@ def _addr(t):
 
 def _launch(dev, where, fn, *args):
     """Call `fn` with the current stream of `dev` as its last argument, `dev` being current."""
-    torch = _torch()
     if dev.type != "cuda":
         raise ValueError(f"{where}: tensors must be on a CUDA device")
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if dev.index == torch.cuda.current_device():
+    torch, index = _torch(), dev.index
+    # the stream as a number: the Stream object would cost 2 us of a call's 12
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if index == torch._C._cuda_getDevice():
         code = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
             code = fn(*args, stream)
-    _check(code, where)
+    if code != OK:
+        raise WinaError(code, where)
 
 
 @dataclass
@@ -558,11 +558,15 @@ class Kv8Cache:
             raise TypeError("k and v must both be int8 or both float8_e4m3fn")
         if k.dim() != 4 or v.shape != k.shape:
             raise ValueError("k and v must be [n_pages][heads][page][dh], of one shape")
-        _on(k.device, k=(k, None), v=(v, None), k_scale=(self.k_scale, torch.float32),
-            v_scale=(self.v_scale, torch.float32))
         n, h, page, dh = k.shape
-        if self.k_scale.shape != (n, h) or self.v_scale.shape != (n, h):
-            raise ValueError("k_scale and v_scale must be [n_pages][heads]")
+        dev = k.device
+        for t in (self.k_scale, self.v_scale):
+            if t.dtype is not torch.float32:
+                raise TypeError("k_scale and v_scale must be float32")
+            if t.shape != (n, h) or not t.is_contiguous() or t.device != dev:
+                raise ValueError(f"k_scale and v_scale must be contiguous [n_pages][heads] on {dev}")
+        if v.device != dev or not k.is_contiguous() or not v.is_contiguous():
+            raise ValueError("k and v must be contiguous and on one device")
         return _Kv8T(k.data_ptr(), v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(), fmt, n, h, page, dh)
 
 
@@ -594,9 +598,8 @@ def kv8_plan(seq_len, new_len, table, free_pages, n_free, page: int, tokens: int
     slots = new(tokens) if slots is None else slots
     positions = new(tokens) if positions is None else positions
     n_free_out = new(1) if n_free_out is None else n_free_out
-    _on(dev, seq_len=(seq_len, i32), new_len=(new_len, i32), table=(table, i32), free_pages=(free_pages, i32),
-        n_free=(n_free, i32), kv_len=(kv_len, i32), cu_q=(cu_q, i32), slots=(slots, i32), positions=(positions, i32),
-        n_free_out=(n_free_out, i32), status=(status, i32))
+    _on(dev, "seq_len new_len table free_pages n_free kv_len cu_q slots positions n_free_out status", seq_len, new_len,
+        table, free_pages, n_free, kv_len, cu_q, slots, positions, n_free_out, status)
     if seq_len.dim() != 1 or new_len.shape != seq_len.shape or table.dim() != 2 or table.shape[0] != B:
         raise ValueError("seq_len and new_len must be [B] and table [B][width]")
     if kv_len.numel() != B or cu_q.numel() != B + 1 or slots.numel() != tokens or positions.numel() != tokens or \
@@ -621,7 +624,6 @@ def _rows(t, name, heads, dh):
 def kv8_write(cache: Kv8Cache, k, v, slots, status=None) -> Kv8Cache:
     """New keys and values [T][heads][dh] (bf16 or float32, rows may be slices of a wider
     tensor's) into the pages of `cache`, at slots int32 [T] (negative: skipped)."""
-    torch = _torch()
     c = cache._struct()
     dev = cache.k.device
     dt = _dt(k)
@@ -630,7 +632,7 @@ def kv8_write(cache: Kv8Cache, k, v, slots, status=None) -> Kv8Cache:
     if k.device != dev or v.device != dev:
         raise ValueError(f"k and v must be on {dev}")
     ld_k, ld_v = _rows(k, "k", c.heads, c.dh), _rows(v, "v", c.heads, c.dh)
-    _on(dev, slots=(slots, torch.int32), status=(status, torch.int32))
+    _on(dev, "slots status", slots, status)
     T = k.shape[0]
     if v.shape[0] != T or slots.numel() != T:
         raise ValueError("k, v and slots must have one length")
@@ -653,9 +655,12 @@ def kv8_read(cache: Kv8Cache, slots, dtype=None, k=None, v=None, status=None):
     dt = _dt(k)
     if dtype is not None and k.dtype != dtype:
         raise TypeError(f"k must be {dtype}")
-    _on(dev, slots=(slots, torch.int32), k=(k, None), v=(v, k.dtype), status=(status, torch.int32))
-    if tuple(k.shape) != shape or tuple(v.shape) != shape:
-        raise ValueError(f"k and v must be {list(shape)}")
+    _on(dev, "slots status", slots, status)
+    if v.dtype is not k.dtype:
+        raise TypeError("k and v must have one dtype")
+    for t in (k, v):
+        if t.shape != shape or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"k and v must be contiguous {list(shape)} on {dev}")
     _launch(dev, "kv8_read", lib.kv8_read, ctypes.byref(c), _addr(slots), T, _addr(k), _addr(v), dt, _addr(status))
     return k, v
 
@@ -668,7 +673,7 @@ def kv8_attention(cache: Kv8Cache, q, table, kv_len, cu_q=None, max_q: int = 1, 
     [T][Hq][dh] in q's dtype; with `out` given, rows behind the last request stay as they were."""
     torch = _torch()
     c = cache._struct()
-    dev, i32 = cache.k.device, torch.int32
+    dev = cache.k.device
     dt = _dt(q)
     if q.device != dev:
         raise ValueError(f"q must be on {dev}")
@@ -679,11 +684,13 @@ def kv8_attention(cache: Kv8Cache, q, table, kv_len, cu_q=None, max_q: int = 1, 
     B = kv_len.numel()
     if out is None:
         out = torch.zeros((T, Hq, c.dh), dtype=q.dtype, device=dev)
-    _on(dev, table=(table, i32), kv_len=(kv_len, i32), cu_q=(cu_q, i32), out=(out, q.dtype), status=(status, i32))
+    _on(dev, "table kv_len cu_q status", table, kv_len, cu_q, status)
+    if out.dtype is not q.dtype:
+        raise TypeError(f"out must be {q.dtype}")
     if table.dim() != 2 or table.shape[0] != B or (cu_q is not None and cu_q.numel() != B + 1):
         raise ValueError("table must be [B][width], kv_len [B] and cu_q [B + 1]")
-    if tuple(out.shape) != (T, Hq, c.dh):
-        raise ValueError(f"out must be {[T, Hq, c.dh]}")
+    if out.shape != (T, Hq, c.dh) or out.device != dev or not out.is_contiguous():
+        raise ValueError(f"out must be contiguous {[T, Hq, c.dh]} on {dev}")
     if Hq < 1 or Hq % c.heads:
         raise ValueError(f"{Hq} query heads over {c.heads} key/value heads")
     if ws is None:

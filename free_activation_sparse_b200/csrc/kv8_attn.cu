@@ -13,6 +13,7 @@
 
 #include "internal.h"
 #include "kv8.cuh"
+#include "tc.cuh"
 
 namespace wina {
 
@@ -34,10 +35,11 @@ struct AttnParams {
   int window;
   void* out;
   int32_t* status;
-  uint32_t* counters;  // [kGridCap], zero between calls
-  float* slots;        // [2 * kGridCap][slot_floats]
+  uint32_t* counters;  // [kMaxTeams], zero between calls
+  float* slots;        // [2 * kMaxTeams][slot_floats]
   int slot_floats;
-  int stages;          // ring depth of k_kv8_attn_split
+  int tiles;      // tiles of query rows, over all heads, at most
+  int tile_cost;  // a tile's fixed cost, in chunks
 };
 
 // ------------------------------------------------------------------------------------
@@ -104,20 +106,26 @@ __device__ __forceinline__ int tiles_of(const AttnParams& p, const Req& r) {
   return (r.nq * p.G + R - 1) / R;
 }
 
-// Chunks of all of a request's tiles, for one kv head.
+// Cost of all of a request's tiles, for one kv head. p.tile_cost is what a tile costs besides
+// its chunks (its queries, the joining of its parts), in chunks; it lies before the tile's
+// first chunk on the line of work.
 template <int R, int CH>
 __device__ __forceinline__ unsigned long long req_cost(const AttnParams& p, const Req& r) {
   const int nt = tiles_of<R>(p, r);
   unsigned long long c = 0;
   for (int t = 0; t < nt; ++t) {
     const Span s = tile_span<R, CH>(p, r, t);
-    c += s.c1 - s.c0;
+    c += s.c1 - s.c0 + p.tile_cost;
   }
   return c;
 }
 
-// Prefix sums over the requests of req_cost, in shared memory (pre[B] the total). Returns
-// false where they pass 32 bits (more than 2^37 keys read: no cache is that large).
+// Prefix sums of req_cost before every fourth request, in shared memory (pre[ceil(B / 4)] the
+// total). Returns false where they pass 32 bits (more than 2^37 keys read: no cache is that
+// large).
+constexpr int kPreStep = 4;
+__host__ __device__ constexpr int pre_entries(int B) { return (B + kPreStep - 1) / kPreStep + 1; }
+
 template <int NTHR, int R, int CH>
 __device__ bool cost_prefix(const AttnParams& p, uint32_t* pre, uint32_t* red) {
   unsigned long long run = 0;
@@ -134,11 +142,11 @@ __device__ bool cost_prefix(const AttnParams& p, uint32_t* pre, uint32_t* red) {
     if (c > 0xffffffffu / NTHR) s_over = 1;  // then the block's sum fits 32 bits below
     uint32_t total;
     const uint32_t ex = block_excl_scan<NTHR>((uint32_t)min(c, (unsigned long long)(0xffffffffu / NTHR)), red, &total);
-    if (b < p.B) pre[b] = (uint32_t)run + ex;
+    if (b < p.B && b % kPreStep == 0) pre[b / kPreStep] = (uint32_t)run + ex;
     run += total;
     if (run > 0xffffffffu) s_over = 1;
   }
-  if (threadIdx.x == 0) pre[p.B] = (uint32_t)run;
+  if (threadIdx.x == 0) pre[pre_entries(p.B) - 1] = (uint32_t)run;
   __syncthreads();
   return s_over == 0;
 }
@@ -149,40 +157,46 @@ struct Walk {
   int b, hk, tile, nt;
   Req r;
   Span s;
-  unsigned long long at;  // chunks before this tile, over all heads
+  unsigned long long at;  // the line's units before this tile
 
+  __device__ __forceinline__ unsigned len(const AttnParams& p) const { return (unsigned)(s.c1 - s.c0 + p.tile_cost); }
+
+  // the tile that holds unit u
   __device__ __forceinline__ void locate(const AttnParams& p, const uint32_t* pre, unsigned long long u) {
-    int lo = 0, hi = p.B;
+    int lo = 0, hi = pre_entries(p.B) - 1;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if ((unsigned long long)pre[mid] * p.c.heads <= u) lo = mid;
       else hi = mid;
     }
-    b = lo;
-    r = load_req(p, b);
+    b = lo * kPreStep;
+    unsigned long long rem = u - (unsigned long long)pre[lo] * p.c.heads, cost;
+    for (;; ++b) {
+      r = load_req(p, b);
+      cost = req_cost<R, CH>(p, r);
+      if (rem < cost * p.c.heads) break;
+      rem -= cost * p.c.heads;
+    }
     nt = tiles_of<R>(p, r);
-    const unsigned cost = pre[b + 1] - pre[b];
-    const unsigned long long rem = u - (unsigned long long)pre[b] * p.c.heads;
     hk = (int)(rem / cost);
     unsigned in = (unsigned)(rem - (unsigned long long)hk * cost);
     tile = 0;
     s = tile_span<R, CH>(p, r, 0);
-    while (in >= (unsigned)(s.c1 - s.c0)) {
-      in -= s.c1 - s.c0;
+    while (in >= len(p)) {
+      in -= len(p);
       s = tile_span<R, CH>(p, r, ++tile);
     }
     at = u - in;
   }
   // to the next tile (there is one)
-  __device__ __forceinline__ void next(const AttnParams& p, const uint32_t* pre) {
-    at += s.c1 - s.c0;
+  __device__ __forceinline__ void next(const AttnParams& p) {
+    at += len(p);
     if (++tile == nt) {
       tile = 0;
       if (++hk == (int)p.c.heads) {
         hk = 0;
-        do ++b;
-        while (b < p.B - 1 && pre[b + 1] == pre[b]);
-        r = load_req(p, b);
+        do r = load_req(p, ++b);
+        while (r.nq == 0 && b < p.B - 1);
         nt = tiles_of<R>(p, r);
       }
     }
@@ -190,32 +204,11 @@ struct Walk {
   }
 };
 
-// The work's [0, C) chunks over nc teams: team i has [C i / nc, C (i + 1) / nc); the team
-// that has chunk u.
+// The line's [0, C) units over nc teams: team i has [C i / nc, C (i + 1) / nc); the team that
+// has unit u.
 __device__ __forceinline__ unsigned long long team_start(unsigned long long C, int nc, int i) { return C * i / nc; }
 __device__ __forceinline__ int team_of(unsigned long long C, int nc, unsigned long long u) {
   return (int)(((u + 1) * nc - 1) / C);
-}
-
-// ------------------------------------------------------------------------------------
-// k_kv8_attn_split
-// ------------------------------------------------------------------------------------
-
-constexpr int kSplitW = 8;                  // warps per CTA
-constexpr int kSplitT = 32 * kSplitW;
-constexpr int kMergeBytes = 16 * 1024;      // merge buffer of a CTA
-constexpr float kPScaleLog2 = 14.f;         // weights are held times 2^14 (float16's middle)
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -224,24 +217,8 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// D += A B, 16 x 8 x 16, float16 operands, float32 accumulators.
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// The transpose of an 8 x 8 matrix of 16-bit elements spread over a warp.
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-
 // The two low (high) bytes of w as float16 numbers. Exact: int8 through 1024 + (byte + 128),
-// whose float16 step is 1; e4m3 is a subset of float16. `biased`: an int8 word already
-// xor-ed with 0x80808080.
+// whose float16 step is 1 (the word already xor-ed by biased()); e4m3 is a subset of float16.
 template <bool E4M3, bool HIGH>
 __device__ __forceinline__ uint32_t half2_of(uint32_t w) {
   if constexpr (E4M3) {
@@ -263,22 +240,87 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Byte offset of 16-byte piece c of row r in a staged tile of DH-byte rows: the pieces are
-// permuted so that both the key reads (8 lanes: 2 rows, 4 pieces) and the value reads (8
+// 16 bytes to shared memory, of which `bytes` are read and the rest zero, under an L2 policy.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes, uint64_t pol) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(bytes), "l"(pol)
+               : "memory");
+}
+
+// Four bytes to shared memory (zeros where `bytes` is 0).
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// ------------------------------------------------------------------------------------
+// k_kv8_attn_split
+// ------------------------------------------------------------------------------------
+
+constexpr int kMaxCtas = 160;               // CTAs, one per SM, at most
+constexpr int kMaxWarps = 12;               // consumer warps of a CTA, at most
+constexpr int kMaxTeams = kMaxCtas * kMaxWarps;
+constexpr int kMaxStages = 4;
+constexpr float kPScaleLog2 = 14.f;         // weights are held times 2^14 (float16's middle)
+
+// D += A B, 16 x 8 x 16, float16 operands, float32 accumulators.
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The transpose of an 8 x 8 matrix of 16-bit elements spread over a warp.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Byte offset of 16-byte piece c of row r in a staged group of 16 rows of DH bytes. The pieces
+// are permuted so that both the key reads (8 lanes: 2 rows, 4 pieces) and the value reads (8
 // lanes: 4 rows, 2 pieces) fall on different banks.
 template <int DH>
 __device__ __forceinline__ uint32_t staged(int r, int c) {
   if constexpr (DH == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-  else return r * DH + ((c ^ (r & 7)) << 4);
+  else return (c >> 3) * 2048 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
-// One CTA of eight warps per SM. The work (tiles of 8 NT query rows of one request and kv
-// head, times the chunks of CH keys they see) is a line cut into equal parts, one per CTA,
-// so that one long sequence fills the GPU and a ragged batch is balanced; a CTA's chunks of
-// one tile go round its warps. Each warp has its own ring of `stages` chunks, filled with
-// cp.async (keys, values and the pages' scales; places outside the tile's keys are filled
-// with zeros and never read), and runs on across tiles, so loads stay in flight while tiles
-// are joined.
+// Four channels of a query row (row = query * G + head in the group): sums over weights.
+template <bool BF16>
+__device__ __forceinline__ void store_row(const AttnParams& p, const Req& r, int hk, int row, int ch, float4 a, float L) {
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const int64_t at = ((int64_t)(r.q0 + row / p.G) * p.Hq + hk * p.G + row % p.G) * p.c.dh + ch;
+  if constexpr (BF16) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(a.x * inv, a.y * inv), y = __floats2bfloat162_rn(a.z * inv, a.w * inv);
+    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + at) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+  } else {
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+  }
+}
+
+// The variants' sizes. The registers set the number of consumer warps (a tile's sums and
+// queries: 16 rows, or rows of 256, or queries in two parts take the most); the shared memory
+// the depth of their rings.
+template <bool BF16, int DH, int NT>
+struct SplitShape {
+  static constexpr int CH = DH == 256 ? 16 : 32;          // keys of a chunk
+  static constexpr int R = 8 * NT;                        // query rows of a tile
+  static constexpr int STAGE = 2 * CH * DH;               // bytes of a chunk, keys and values
+  static constexpr int NCW = NT * DH == 256 ? 8 : 12;     // warps: 168 or 255 registers a thread
+  static constexpr int THREADS = 32 * NCW;
+  static constexpr int S = DH == 64 ? 4 : NCW == 8 ? 3 : 2;  // chunks of a warp's ring
+  static constexpr int RPR = DH == 256 ? 2 : 4;           // rows joined at a time
+  static constexpr int MERGE = NCW * RPR * DH * 4;        // bytes of the merge buffer
+  static constexpr size_t SMEM = (size_t)NCW * S * STAGE + MERGE;
+};
+
+// One CTA per SM: consumer warps, and one warp whose lane w feeds consumer warp w. The work
+// (tiles of 8 NT query rows of one request and kv head, times the chunks of CH keys they see)
+// is a line cut into equal parts, one for each team, so that one long sequence fills the GPU
+// and a ragged batch is balanced. A team is a whole CTA, whose warps take a tile's chunks in
+// turn (few tiles), or one warp (many tiles, whose fixed costs then run side by side). Each
+// warp has its own ring of chunks, filled by tensor copies of 16 keys; the feeding lane runs on
+// across tiles, so loads stay in flight while tiles are joined.
 //
 // Per chunk, with keys as the rows of the matrix instruction, so that 8 query rows cost half
 // of what 16 do:
@@ -290,131 +332,168 @@ __device__ __forceinline__ uint32_t staged(int r, int c) {
 //   O^T += V^T P^T with P = p vs / sref in float16 (float32: two parts), sref the largest
 //                 value scale met so far: a weight keeps 11 (22) bits down to 2^-28 of the
 //                 largest, and O is rescaled where max or sref grow.
-// The eight warps' (max, sum, O) are joined in shared memory in warp order; a tile cut by a
-// part's end is left in the workspace, and the last CTA of that tile to arrive joins the
-// parts in order. No CTA waits for another.
-template <bool BF16, bool E4M3, int DH, int NT>
-__global__ void __launch_bounds__(kSplitT, 1) k_kv8_attn_split(AttnParams p) {
-  constexpr int CH = DH == 256 ? 16 : 32;     // keys of a chunk
+// The bytes' conversion and the softmax, some 420 instructions a chunk of 32 keys in one
+// dependent stream, are what a warp spends its time on; eleven warps hide its latency.
+// A team's warps' (max, sum, O) are joined in shared memory in warp order; a tile cut by a
+// part's end is left in the workspace, and the last team of that tile to arrive joins the
+// parts in order. No team waits for another.
+template <bool BF16, bool E4M3, int DH, int NT, bool WARPS>
+__global__ void __launch_bounds__(SplitShape<BF16, DH, NT>::THREADS, 1)
+    k_kv8_attn_split(const AttnParams p) {
+  using Sh = SplitShape<BF16, DH, NT>;
+  constexpr int CH = Sh::CH, R = Sh::R, STAGE = Sh::STAGE, NCW = Sh::NCW, S = Sh::S, RPR = Sh::RPR;
+  constexpr int TEAM = WARPS ? 1 : NCW;       // warps of a team
   constexpr int MT = CH / 16;                 // 16-key groups of a chunk
-  constexpr int R = 8 * NT;                   // query rows of a tile
   constexpr int KS = DH / 16;                 // k-steps of a score, and 16-channel tiles of O
   constexpr int KC = DH / 64;                 // 16-byte pieces of a key row per lane
   constexpr int PARTS = BF16 ? 1 : 2;
-  constexpr int STAGE = 2 * CH * DH;
   extern __shared__ __align__(128) unsigned char sm[];
   __shared__ uint32_t red[32];
-  __shared__ float s_m[kSplitW][R], s_l[kSplitW][R];
-  __shared__ float s_meta[kSplitW][3][4];     // ks, vs of a chunk's 16-key groups
-  __shared__ uint32_t s_bad[kSplitW][3];
+  __shared__ float s_m[NCW][R], s_l[NCW][R];
+  __shared__ float s_meta[NCW][S][4];         // ks, vs of a chunk's 16-key groups
+  __shared__ uint32_t s_bad[NCW][S];
   __shared__ uint32_t s_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const int S = p.stages;
-  unsigned char* ring = sm + (size_t)warp * S * STAGE;
-  float* mbuf = reinterpret_cast<float*>(sm + (size_t)kSplitW * S * STAGE);
-  uint32_t* pre = reinterpret_cast<uint32_t*>(sm + (size_t)kSplitW * S * STAGE + kMergeBytes);
-  if (!cost_prefix<kSplitT, R, CH>(p, pre, red)) {
+  float* mbuf = reinterpret_cast<float*>(sm + (size_t)NCW * S * STAGE);
+  uint32_t* pre = reinterpret_cast<uint32_t*>(sm + (size_t)NCW * S * STAGE + Sh::MERGE);
+  if (!cost_prefix<Sh::THREADS, R, CH>(p, pre, red)) {
     if (blockIdx.x == 0 && tid == 0) record_status(p.status, WINA_ERR_INVALID_ARG);
     return;
   }
-  const unsigned long long C = (unsigned long long)pre[p.B] * p.c.heads;
+  const unsigned long long C = (unsigned long long)pre[pre_entries(p.B) - 1] * p.c.heads;
   if (C == 0) return;
-  // at least one chunk for each warp of a team
-  const int nc = (int)min((unsigned long long)gridDim.x, (C + kSplitW - 1) / kSplitW);
-  if ((int)blockIdx.x >= nc) return;
-  const unsigned long long u0 = team_start(C, nc, blockIdx.x), u1 = team_start(C, nc, blockIdx.x + 1);
+  // The number of teams. A CTA that gets parts of two tiles pays a tile's fixed cost twice, so
+  // with fewer tiles than CTAs it is a multiple of the tiles (each of equal tiles is then cut
+  // alike, and no CTA has parts of two) unless that leaves too many idle; a part is worth at
+  // least a chunk for each of the CTA's warps. (One sequence of 4096 tokens, 32 heads: 18.6 us
+  // on all SMs, 16.7 on 128 of them.)
+  const int teams = gridDim.x * (NCW / TEAM);
+  int nc = teams;
+  if (!WARPS && p.tiles <= teams) {
+    const int k = (int)max(1ull, min((unsigned long long)(teams / p.tiles), (C / p.tiles + TEAM / 2) / TEAM));
+    const int even = p.tiles * k;
+    nc = (int)min((unsigned long long)teams, max((unsigned long long)p.tiles, C / TEAM));
+    if (C / even <= C / nc + 20) nc = even;
+  }
+  nc = (int)min((unsigned long long)nc, C);  // every team has a unit, so that a tile's parts can be counted
+  const int team = WARPS ? warp * gridDim.x + blockIdx.x : blockIdx.x, member = WARPS ? 0 : warp;
+  if (team >= nc) return;
+  const unsigned long long u0 = team_start(C, nc, team), u1 = team_start(C, nc, team + 1);
 
   using W = Walk<R, CH>;
-  W cons, prod;  // the tile being computed, the tile being loaded
-  cons.locate(p, pre, u0);
-  prod = cons;
-  // the chunks [from, to) of a tile that this CTA has; this warp's are from + warp, + 8, ...
+  // the chunks [from, to) of a tile that this team has (none where its part of the line ends in
+  // the tile's fixed cost); this warp's are from + member, + TEAM, ...
   auto part = [&](const W& w, int& from, int& to) {
-    from = w.s.c0 + (int)(u0 > w.at ? u0 - w.at : 0);
-    const unsigned long long end = w.at + (unsigned)(w.s.c1 - w.s.c0);
-    to = end > u1 ? w.s.c1 - (int)(end - u1) : w.s.c1;
+    const unsigned long long first = w.at + p.tile_cost, end = w.at + w.len(p);
+    from = w.s.c0 + (int)(u0 > first ? u0 - first : 0);
+    to = u1 >= end ? w.s.c1 : u1 > first ? w.s.c0 + (int)(u1 - first) : w.s.c0;
   };
-  int pc, pto;  // the producer's next chunk
-  part(prod, pc, pto);
-  pc += warp;
-  bool more = true;
-  // page indices of the producer's next chunks, one chunk to a lane
-  int pg0 = -1, pg1 = -1, pg_from = -1, pg_b = -1;
+  W w;  // the tile being computed
+  w.locate(p, pre, u0);
 
+  // ---- loading: the warp's next chunk, tile after tile ----
+  // (the walk lies in shared memory: it is looked at when a tile ends, and would cost registers)
+  __shared__ W s_walk[NCW];
+  const uint64_t pol = l2_evict_first_policy();
   const int page_mask = (1 << p.shift) - 1;
-  // issue the next chunk of this warp into `stage`
-  auto issue = [&](int stage) {
+  int pc, pto, plo, phi, phk;       // its chunk, and its tile's end, keys and head
+  int pg0 = -1, pg1 = -1, pg_from;  // page indices of its tile's next chunks, one chunk to a lane
+  bool more = true;
+  auto load_pages = [&](const W& v) {
+    pg_from = pc;
+    const int64_t key = (int64_t)(pc + lane * TEAM) * CH;
+    const int32_t* row = p.table + (int64_t)v.b * p.width;
+    pg0 = key < v.s.hi && key + 16 > v.s.lo ? __ldg(row + (key >> p.shift)) : -1;
+    if (MT == 2) pg1 = key + 16 < v.s.hi && key + 32 > v.s.lo ? __ldg(row + ((key + 16) >> p.shift)) : -1;
+  };
+  auto enter = [&](const W& v) {
+    part(v, pc, pto);
+    pc += member;
+    plo = v.s.lo;
+    phi = v.s.hi;
+    phk = v.hk;
+    load_pages(v);
+    // the tile's queries, towards L2
+    constexpr int LINES = DH * (BF16 ? 2 : 4) / 128;
+    for (int i = member * 32 + lane; i < R * LINES; i += TEAM * 32) {
+      const int rr = v.tile * R + i / LINES;
+      if (rr < v.r.nq * p.G) {
+        const int64_t at = (int64_t)(v.r.q0 + rr / p.G) * p.ld_q + (int64_t)(v.hk * p.G + rr % p.G) * DH;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(p.q) + at * (BF16 ? 2 : 4) + (i % LINES) * 128));
+      }
+    }
+  };
+  enter(w);
+  if (lane == 0) s_walk[warp] = w;
+  __syncwarp();
+  // one chunk into `slot`
+  auto issue = [&](int slot) {
     while (more && pc >= pto) {  // the next tile with a chunk for this warp
-      if (prod.at + (unsigned)(prod.s.c1 - prod.s.c0) >= u1) {
+      W v = s_walk[warp];
+      __syncwarp();
+      if (v.at + v.len(p) >= u1) {
         more = false;
         break;
       }
-      prod.next(p, pre);
-      part(prod, pc, pto);
-      pc += warp;
+      v.next(p);
+      enter(v);
+      if (lane == 0) s_walk[warp] = v;
+      __syncwarp();
     }
     if (more) {
-      const int off = pc - pg_from;
-      if (pg_b != prod.b || off < 0 || off >= 32 * kSplitW || (off & (kSplitW - 1))) {
-        pg_b = prod.b;
-        pg_from = pc;
-        const int64_t key = (int64_t)(pc + lane * kSplitW) * CH;
-        const int32_t* row = p.table + (int64_t)prod.b * p.width;
-        pg0 = key < prod.r.kv ? __ldg(row + (key >> p.shift)) : -1;
-        if (MT == 2) pg1 = key + 16 < prod.r.kv ? __ldg(row + ((key + 16) >> p.shift)) : -1;
-      }
-      const int from = (pc - pg_from) / kSplitW;
-      const int key0 = pc * CH;
-      int64_t head[MT];  // (page, head) of each 16-key group, in rows of the cache
+      if (pc - pg_from == 32 * TEAM) load_pages(s_walk[warp]);
+      const int src = (pc - pg_from) / TEAM, key0 = pc * CH;
       uint32_t bad = 0;
+      int64_t head[MT];  // (page, head) of each 16-key group, -1 where none is read
 #pragma unroll
       for (int u = 0; u < MT; ++u) {
-        const int pg = __shfl_sync(0xffffffffu, u ? pg1 : pg0, from);
-        const bool used = key0 + 16 * u < prod.s.hi && key0 + 16 * u + 16 > prod.s.lo;
-        const bool ok = used && pg >= 0 && pg < p.c.n_pages;
-        head[u] = ok ? (int64_t)pg * p.c.heads + prod.hk : -1;
-        if (used && !ok) {
-          bad |= 1u << u;
-          if (lane == 0) record_status(p.status, WINA_ERR_INVALID_ARG);
-        }
+        const int pg = __shfl_sync(0xffffffffu, u ? pg1 : pg0, src);
+        const bool used = key0 + 16 * u < phi && key0 + 16 * u + 16 > plo, ok = used && pg >= 0 && pg < p.c.n_pages;
+        head[u] = ok ? (int64_t)pg * p.c.heads + phk : -1;
+        if (used && !ok) bad |= 1u << u;
       }
-      const uint32_t dst = (uint32_t)__cvta_generic_to_shared(ring + (size_t)stage * STAGE);
-      constexpr int PPR = DH / 16;  // pieces per row
+      if (bad && lane == 0) record_status(p.status, WINA_ERR_INVALID_ARG);
+      const uint32_t dst = tc::smem_u32(sm + (size_t)(warp * S + slot) * STAGE);
+      constexpr int PPR = DH / 16;  // 16-byte pieces per row
 #pragma unroll
       for (int i = 0; i < CH * PPR / 32; ++i) {
-        const int piece = i * 32 + lane, row = piece / PPR, c = piece % PPR, key = key0 + row;
-        const int64_t h = head[MT == 2 ? (i * 32 / PPR) / 16 : 0];  // a pass stays in one group
-        const bool on = h >= 0 && key >= prod.s.lo && key < prod.s.hi;
-        const int64_t src = on ? ((h << p.shift) + (key & page_mask)) * DH + c * 16 : 0;
-        const uint32_t d = dst + staged<DH>(row, c);
-        cp_async16(d, reinterpret_cast<const uint8_t*>(p.c.k) + src, on ? 16 : 0);
-        cp_async16(d + CH * DH, reinterpret_cast<const uint8_t*>(p.c.v) + src, on ? 16 : 0);
+        const int piece = i * 32 + lane, row = piece / PPR, key = key0 + row;
+        const int64_t h = head[MT == 2 ? (i * 32 / PPR) / 16 : 0];  // the 32 pieces lie in one group
+        const bool on = h >= 0 && key >= plo && key < phi;
+        const int64_t from = on ? ((h << p.shift) + (key & page_mask)) * DH + (piece % PPR) * 16 : 0;
+        const uint32_t d = dst + (row / 16) * 16 * DH + staged<DH>(row % 16, piece % PPR);
+        cp_async16(d, reinterpret_cast<const uint8_t*>(p.c.k) + from, on ? 16 : 0, pol);
+        cp_async16(d + CH * DH, reinterpret_cast<const uint8_t*>(p.c.v) + from, on ? 16 : 0, pol);
       }
       if (lane < 2 * MT) {
         const int64_t h = (MT == 2 && (lane & 1)) ? head[MT - 1] : head[0];
-        const float* s = (lane >= MT ? p.c.v_scale : p.c.k_scale) + (h >= 0 ? h : 0);
-        cp_async4((uint32_t)__cvta_generic_to_shared(&s_meta[warp][stage][lane]), s, h >= 0 ? 4 : 0);
+        cp_async4(tc::smem_u32(&s_meta[warp][slot][lane]), (lane >= MT ? p.c.v_scale : p.c.k_scale) + (h >= 0 ? h : 0), h >= 0 ? 4 : 0);
       }
-      if (lane == 0) s_bad[warp][stage] = bad;
-      pc += kSplitW;
+      if (lane == 0) s_bad[warp][slot] = bad;
+      pc += TEAM;
     }
-    cp_commit();
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-
+#pragma unroll
   for (int i = 0; i < S - 1; ++i) issue(i);
-  int stage = 0;
 
+  int it = 0;
   for (;;) {  // tiles
     int from, to;
-    part(cons, from, to);
-    const int rows = min(R, cons.r.nq * p.G - cons.tile * R);
+    part(w, from, to);
+    if (from >= to) {
+      if (w.at + w.len(p) >= u1) break;
+      w.next(p);
+      continue;
+    }
+    const int rows = min(R, w.r.nq * p.G - w.tile * R);
     // queries: lane (g, t) has row g's pieces of channels as the keys' lanes t have them
     uint32_t qf[PARTS][NT][KS][2];
     float cr[NT][2];  // factor of a score, rows 2t and 2t + 1
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int row = nt * 8 + g, rr = cons.tile * R + row;
-      const int64_t at = (int64_t)(cons.r.q0 + rr / p.G) * p.ld_q + (int64_t)(cons.hk * p.G + rr % p.G) * DH;
+      const int row = nt * 8 + g, rr = w.tile * R + row;
+      const int64_t at = (int64_t)(w.r.q0 + rr / p.G) * p.ld_q + (int64_t)(w.hk * p.G + rr % p.G) * DH;
       float f[KC][16], big = 0.f;
 #pragma unroll
       for (int j = 0; j < KC; ++j) {
@@ -442,34 +521,25 @@ __global__ void __launch_bounds__(kSplitT, 1) k_kv8_attn_split(AttnParams p) {
 #pragma unroll
       for (int j = 0; j < KC; ++j)
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
+        for (int k = 0; k < 4; ++k)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float x = f[j][4 * w + 2 * e] * up, y = f[j][4 * w + 2 * e + 1] * up;
+            const float x = f[j][4 * k + 2 * e] * up, y = f[j][4 * k + 2 * e + 1] * up;
             const __half2 h = __floats2half2_rn(x, y);
-            qf[0][nt][j * 4 + w][e] = *reinterpret_cast<const uint32_t*>(&h);
+            qf[0][nt][j * 4 + k][e] = *reinterpret_cast<const uint32_t*>(&h);
             if constexpr (!BF16) {
               const float2 back = __half22float2(h);
-              qf[PARTS - 1][nt][j * 4 + w][e] = pack_half2(x - back.x, y - back.y);
+              qf[PARTS - 1][nt][j * 4 + k][e] = pack_half2(x - back.x, y - back.y);
             }
           }
       const float fac = dn * p.scale * (p.softcap > 0.f ? 1.f / p.softcap : kLog2e);
       cr[nt][0] = __shfl_sync(0xffffffffu, fac, 8 * t);
       cr[nt][1] = __shfl_sync(0xffffffffu, fac, 8 * t + 4);
     }
-    // rows 2t, 2t + 1 (+ 8): the keys they see
-    int lim[NT][2], low[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int rr = cons.tile * R + min(nt * 8 + 2 * t + e, rows - 1);
-        lim[nt][e] = cons.r.kv - cons.r.n + rr / p.G + 1;
-        low[nt][e] = p.window > 0 ? lim[nt][e] - p.window : 0;
-      }
     // chunks between these need no masks
-    const int first_lim = cons.r.kv - cons.r.n + cons.tile * R / p.G + 1;
-    const int last_low = p.window > 0 ? cons.r.kv - cons.r.n + (cons.tile * R + rows - 1) / p.G + 1 - p.window : 0;
+    const int pos0 = w.r.kv - w.r.n;
+    const int first_lim = pos0 + w.tile * R / p.G + 1;
+    const int last_low = max(w.s.lo, p.window > 0 ? pos0 + (w.tile * R + rows - 1) / p.G + 1 - p.window : 0);
 
     float o[NT][KS][4], m[NT][2], l[NT][2], sref = 1.17549435e-38f, inv_sref = 1.f / 1.17549435e-38f;
 #pragma unroll
@@ -482,12 +552,12 @@ __global__ void __launch_bounds__(kSplitT, 1) k_kv8_attn_split(AttnParams p) {
       l[nt][0] = l[nt][1] = 0.f;
     }
 
-    for (int c = from + warp; c < to; c += kSplitW) {
-      if (S == 3) cp_wait<1>();
-      else cp_wait<0>();
-      __syncwarp();
-      issue(stage == 0 ? S - 1 : stage - 1);
-      const unsigned char* kst = ring + (size_t)stage * STAGE;
+    for (int c = from + member; c < to; c += TEAM, ++it) {
+      const int slot = it % S;
+      asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+      __syncwarp();  // everybody's pieces are there, and the slot before this one is read
+      issue((it + S - 1) % S);
+      const unsigned char* kst = sm + (size_t)(warp * S + slot) * STAGE;
       const unsigned char* vst = kst + CH * DH;
       float s[NT][MT][4];
 #pragma unroll
@@ -501,29 +571,29 @@ __global__ void __launch_bounds__(kSplitT, 1) k_kv8_attn_split(AttnParams p) {
 #pragma unroll
         for (int j = 0; j < KC; ++j) {
           const int cc = DH == 64 ? t : (j >> 1) * 8 + 2 * t + (j & 1);
-          const uint4 x = *reinterpret_cast<const uint4*>(kst + staged<DH>(u * 16 + g, cc));
-          const uint4 y = *reinterpret_cast<const uint4*>(kst + staged<DH>(u * 16 + g + 8, cc));
+          const uint4 x = *reinterpret_cast<const uint4*>(kst + u * 16 * DH + staged<DH>(g, cc));
+          const uint4 y = *reinterpret_cast<const uint4*>(kst + u * 16 * DH + staged<DH>(g + 8, cc));
           const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint32_t a = biased<E4M3>(xs[w]), b = biased<E4M3>(ys[w]);
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t a = biased<E4M3>(xs[k]), b = biased<E4M3>(ys[k]);
             const uint32_t fr[4] = {half2_of<E4M3, false>(a), half2_of<E4M3, false>(b), half2_of<E4M3, true>(a),
                                     half2_of<E4M3, true>(b)};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int q = 0; q < PARTS; ++q) mma16816(s[nt][u], fr, qf[q][nt][j * 4 + w][0], qf[q][nt][j * 4 + w][1]);
+              for (int q = 0; q < PARTS; ++q) mma16816(s[nt][u], fr, qf[q][nt][j * 4 + k][0], qf[q][nt][j * 4 + k][1]);
           }
         }
       float ks[MT], vs[MT];
 #pragma unroll
       for (int u = 0; u < MT; ++u) {
-        ks[u] = s_meta[warp][stage][u];
-        vs[u] = s_meta[warp][stage][MT + u];
+        ks[u] = s_meta[warp][slot][u];
+        vs[u] = s_meta[warp][slot][MT + u];
       }
-      const uint32_t bad = s_bad[warp][stage];
+      const uint32_t bad = s_bad[warp][slot];
       const int key0 = c * CH;
-      const bool masked = bad || key0 < last_low || key0 < cons.s.lo || key0 + CH > first_lim;
+      const bool masked = bad || key0 < last_low || key0 + CH > first_lim;
       // scores in units of log 2
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -539,12 +609,18 @@ __global__ void __launch_bounds__(kSplitT, 1) k_kv8_attn_split(AttnParams p) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int u = 0; u < MT; ++u)
+          for (int e = 0; e < 2; ++e) {
+            // the keys that row 2t + e sees
+            const int lim = pos0 + (w.tile * R + min(nt * 8 + 2 * t + e, rows - 1)) / p.G + 1;
+            const int low = p.window > 0 ? lim - p.window : 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int key = key0 + 16 * u + g + (e >> 1) * 8;
-              if (key >= lim[nt][e & 1] || key < low[nt][e & 1] || ((bad >> u) & 1)) s[nt][u][e] = -INFINITY;
-            }
+            for (int u = 0; u < MT; ++u)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int key = key0 + 16 * u + g + h * 8;
+                if (key >= lim || key < low || ((bad >> u) & 1)) s[nt][u][2 * h + e] = -INFINITY;
+              }
+          }
       }
       bool grew = false;
       float mb[NT][2], al[NT][2];
@@ -567,12 +643,12 @@ __global__ void __launch_bounds__(kSplitT, 1) k_kv8_attn_split(AttnParams p) {
 #pragma unroll
       for (int u = 0; u < MT; ++u) {
         const float a = fabsf(vs[u]);
-        if (a < INFINITY && !((bad >> u) & 1)) vmax = fmaxf(vmax, a);
+        if (a < INFINITY) vmax = fmaxf(vmax, a);
       }
       if (__any_sync(0xffffffffu, grew) || vmax > sref) {
-        const float down = sref * __fdiv_rn(1.f, vmax);
-        sref = vmax;
         inv_sref = __fdiv_rn(1.f, vmax);
+        const float down = sref * inv_sref;
+        sref = vmax;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -589,21 +665,21 @@ __global__ void __launch_bounds__(kSplitT, 1) k_kv8_attn_split(AttnParams p) {
         const float ratio = vs[u] * inv_sref;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float w[4];
+          float x[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            w[e] = ex2(s[nt][u][e] - mb[nt][e & 1]);
-            l[nt][e & 1] += w[e];
+            x[e] = ex2(s[nt][u][e] - mb[nt][e & 1]);
+            l[nt][e & 1] += x[e];
             // a weight of 0 stays 0 under any scale
-            w[e] = w[e] == 0.f ? 0.f : w[e] * ratio;
+            x[e] = x[e] == 0.f ? 0.f : x[e] * ratio;
           }
-          const __half2 a = __floats2half2_rn(w[0], w[1]), b = __floats2half2_rn(w[2], w[3]);
+          const __half2 a = __floats2half2_rn(x[0], x[1]), b = __floats2half2_rn(x[2], x[3]);
           pf[0][nt][u][0] = transpose8x8(*reinterpret_cast<const uint32_t*>(&a));
           pf[0][nt][u][1] = transpose8x8(*reinterpret_cast<const uint32_t*>(&b));
           if constexpr (!BF16) {
             const float2 fa = __half22float2(a), fb = __half22float2(b);
-            pf[PARTS - 1][nt][u][0] = transpose8x8(pack_half2(w[0] - fa.x, w[1] - fa.y));
-            pf[PARTS - 1][nt][u][1] = transpose8x8(pack_half2(w[2] - fb.x, w[3] - fb.y));
+            pf[PARTS - 1][nt][u][0] = transpose8x8(pack_half2(x[0] - fa.x, x[1] - fa.y));
+            pf[PARTS - 1][nt][u][1] = transpose8x8(pack_half2(x[2] - fb.x, x[3] - fb.y));
           }
         }
       }
@@ -615,40 +691,44 @@ __global__ void __launch_bounds__(kSplitT, 1) k_kv8_attn_split(AttnParams p) {
           uint32_t x[4][VW];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int row = u * 16 + 2 * t + (k & 1) + (k >> 1) * 8;
+            const int row = 2 * t + (k & 1) + (k >> 1) * 8;
             if constexpr (DH == 64) {
-              const uint2 v = *reinterpret_cast<const uint2*>(vst + staged<DH>(row, g >> 1) + (g & 1) * 8);
-              x[k][0] = biased<E4M3>(v.x);
-              x[k][1] = biased<E4M3>(v.y);
+              const uint2 v = *reinterpret_cast<const uint2*>(vst + u * 16 * DH + staged<DH>(row, g >> 1) + (g & 1) * 8);
+              x[k][0] = v.x;
+              x[k][1] = v.y;
             } else {
-              const uint4 v = *reinterpret_cast<const uint4*>(vst + staged<DH>(row, h * 8 + g));
-              x[k][0] = biased<E4M3>(v.x);
-              x[k][1] = biased<E4M3>(v.y);
-              x[k][2] = biased<E4M3>(v.z);
-              x[k][3] = biased<E4M3>(v.w);
+              const uint4 v = *reinterpret_cast<const uint4*>(vst + u * 16 * DH + staged<DH>(row, h * 8 + g));
+              x[k][0] = v.x;
+              x[k][1] = v.y;
+              x[k][2] = v.z;
+              x[k][3] = v.w;
             }
+#pragma unroll
+            for (int q = 0; q < VW; ++q) x[k][q] = biased<E4M3>(x[k][q]);
           }
 #pragma unroll
-          for (int w = 0; w < VW; ++w) {
-            // channels 4w, 4w + 1 of two keys side by side, then 4w + 2, 4w + 3
+          for (int q = 0; q < VW; ++q) {
+            // channels 4q, 4q + 1 of two keys side by side, then 4q + 2, 4q + 3
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const uint32_t a = __byte_perm(x[0][w], x[1][w], e ? 0x7362 : 0x5140);
-              const uint32_t b = __byte_perm(x[2][w], x[3][w], e ? 0x7362 : 0x5140);
+              const uint32_t a = __byte_perm(x[0][q], x[1][q], e ? 0x7362 : 0x5140);
+              const uint32_t b = __byte_perm(x[2][q], x[3][q], e ? 0x7362 : 0x5140);
               const uint32_t fr[4] = {half2_of<E4M3, false>(a), half2_of<E4M3, true>(a), half2_of<E4M3, false>(b),
                                       half2_of<E4M3, true>(b)};
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int q = 0; q < PARTS; ++q)
-                  mma16816(o[nt][h * 8 + 2 * w + e], fr, pf[q][nt][u][0], pf[q][nt][u][1]);
+                for (int i = 0; i < PARTS; ++i)
+                  mma16816(o[nt][h * 8 + 2 * q + e], fr, pf[i][nt][u][0], pf[i][nt][u][1]);
             }
           }
         }
-      stage = stage == S - 1 ? 0 : stage + 1;
     }
 
     // ---- join the warps' parts of this tile ----
+    const bool whole = from == w.s.c0 && to == w.s.c1;
+    // this team's slot: a part that begins its tile elsewhere comes first
+    float* slot = p.slots + (size_t)(2 * team + (from == w.s.c0 ? 1 : 0)) * p.slot_floats;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -657,140 +737,138 @@ __global__ void __launch_bounds__(kSplitT, 1) k_kv8_attn_split(AttnParams p) {
         x += __shfl_xor_sync(0xffffffffu, x, 4);
         x += __shfl_xor_sync(0xffffffffu, x, 8);
         x += __shfl_xor_sync(0xffffffffu, x, 16);
-        if (g == 0) {
+        l[nt][e] = x;
+        if (!WARPS && g == 0) {
           s_m[warp][nt * 8 + 2 * t + e] = m[nt][e];
           s_l[warp][nt * 8 + 2 * t + e] = x;
         }
       }
-    __syncthreads();
-    const bool whole = from == cons.s.c0 && to == cons.s.c1;
-    // this CTA's slot: a part that begins its tile elsewhere comes first
-    float* slot = p.slots + (size_t)(2 * blockIdx.x + (from == cons.s.c0 ? 1 : 0)) * p.slot_floats;
-    float fac[NT][2];
+    constexpr int CPL = DH == 64 ? 8 : 16;  // consecutive channels a lane has (of each 128)
+    if constexpr (WARPS) {
+      // lane (g, t): rows 2t, 2t + 1, channels g * CPL ..
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = nt * 8 + 2 * t + e;
-        float M = -INFINITY;
-        for (int w = 0; w < kSplitW; ++w) M = fmaxf(M, s_m[w][row]);
-        fac[nt][e] = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - M) * sref;
-      }
-    // rounds of RC channels of 8 rows
-    constexpr int RC = kMergeBytes / (kSplitW * 8 * 4) < DH ? kMergeBytes / (kSplitW * 8 * 4) : DH;
-    constexpr int CPL = DH == 64 ? 8 : 16;  // consecutive channels a lane has of a 128-channel half
+        for (int e = 0; e < 2; ++e) {
+          const int row = nt * 8 + 2 * t + e;
+          if (row >= rows) continue;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+          for (int h = 0; h < (DH == 256 ? 2 : 1); ++h)
 #pragma unroll
-      for (int c0 = 0; c0 < DH; c0 += RC) {
-        // lane (g, t): rows 2t, 2t + 1, channels g * CPL .. (+ 128 for the second half)
+            for (int q = 0; q < CPL / 4; ++q) {
+              const int ch = h * 128 + g * CPL + 4 * q;
+              const float4 a = make_float4(o[nt][h * 8 + 2 * q][e] * sref, o[nt][h * 8 + 2 * q][e + 2] * sref,
+                                           o[nt][h * 8 + 2 * q + 1][e] * sref, o[nt][h * 8 + 2 * q + 1][e + 2] * sref);
+              if (whole) store_row<BF16>(p, w.r, w.hk, w.tile * R + row, ch, a, l[nt][e]);
+              else *reinterpret_cast<float4*>(slot + (size_t)row * DH + ch) = a;
+            }
+          if (!whole && g == 0) {
+            slot[R * DH + row] = m[nt][e];
+            slot[R * DH + R + row] = l[nt][e];
+          }
+        }
+    }
+    // rounds of RPR rows
+    for (int r0 = 0; !WARPS && r0 < rows; r0 += RPR) {
 #pragma unroll
-        for (int h = 0; h < (DH == 256 ? 2 : 1); ++h) {
-          const int ch = h * 128 + g * CPL;
-          if (ch >= c0 && ch < c0 + RC) {
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float* d = mbuf + ((size_t)warp * 8 + 2 * t + e) * RC + (ch - c0);
+        for (int e = 0; e < 2; ++e) {
+          const int row = nt * 8 + 2 * t + e;  // lane (g, t): rows 2t, 2t + 1, channels g * CPL ..
+          if (row >= r0 && row < r0 + RPR && row < rows) {
+#pragma unroll
+            for (int h = 0; h < (DH == 256 ? 2 : 1); ++h) {
+              float* d = mbuf + ((size_t)warp * RPR + row - r0) * DH + h * 128 + g * CPL;
 #pragma unroll
               for (int q = 0; q < CPL / 4; ++q)
                 *reinterpret_cast<float4*>(d + 4 * q) =
-                    make_float4(o[nt][h * 8 + 2 * q][e] * fac[nt][e], o[nt][h * 8 + 2 * q][e + 2] * fac[nt][e],
-                                o[nt][h * 8 + 2 * q + 1][e] * fac[nt][e], o[nt][h * 8 + 2 * q + 1][e + 2] * fac[nt][e]);
+                    make_float4(o[nt][h * 8 + 2 * q][e] * sref, o[nt][h * 8 + 2 * q][e + 2] * sref,
+                                o[nt][h * 8 + 2 * q + 1][e] * sref, o[nt][h * 8 + 2 * q + 1][e + 2] * sref);
             }
           }
         }
-        __syncthreads();
-        for (int i = tid; i < 8 * RC / 4; i += kSplitT) {
-          const int row = i / (RC / 4), ch = (i % (RC / 4)) * 4, rr = nt * 8 + row;
-          if (rr >= rows) continue;
-          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      __syncthreads();
+      for (int i = tid; i < min(RPR, rows - r0) * DH / 4; i += 32 * NCW) {
+        const int row = i / (DH / 4), ch = (i % (DH / 4)) * 4, rr = r0 + row;
+        float M = -INFINITY, L = 0.f;
 #pragma unroll
-          for (int w = 0; w < kSplitW; ++w) {
-            const float4 x = *reinterpret_cast<const float4*>(mbuf + ((size_t)w * 8 + row) * RC + ch);
-            a.x += x.x;
-            a.y += x.y;
-            a.z += x.z;
-            a.w += x.w;
-          }
-          if (whole) {
-            float M = -INFINITY, L = 0.f;
-            for (int w = 0; w < kSplitW; ++w) M = fmaxf(M, s_m[w][rr]);
-            for (int w = 0; w < kSplitW; ++w) L += s_m[w][rr] == -INFINITY ? 0.f : s_l[w][rr] * ex2(s_m[w][rr] - M);
-            const float inv = L == 0.f ? 0.f : 1.f / L;
-            const int qr = cons.tile * R + rr;
-            const int64_t at = ((int64_t)(cons.r.q0 + qr / p.G) * p.Hq + cons.hk * p.G + qr % p.G) * DH + c0 + ch;
-            if constexpr (BF16) {
-              const __nv_bfloat162 x = __floats2bfloat162_rn(a.x * inv, a.y * inv), y = __floats2bfloat162_rn(a.z * inv, a.w * inv);
-              *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + at) =
-                  make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-            } else {
-              *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at) =
-                  make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-            }
-          } else {
-            *reinterpret_cast<float4*>(slot + (size_t)rr * DH + c0 + ch) = a;
+        for (int k = 0; k < NCW; ++k) M = fmaxf(M, s_m[k][rr]);
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < NCW; ++k) {
+          const float mk = s_m[k][rr], f = mk == -INFINITY ? 0.f : ex2(mk - M);
+          if (f == 0.f) continue;  // a warp without keys, or without weight
+          const float4 x = *reinterpret_cast<const float4*>(mbuf + ((size_t)k * RPR + row) * DH + ch);
+          L += s_l[k][rr] * f;
+          a.x += x.x * f;
+          a.y += x.y * f;
+          a.z += x.z * f;
+          a.w += x.w * f;
+        }
+        if (whole) {
+          store_row<BF16>(p, w.r, w.hk, w.tile * R + rr, ch, a, L);
+        } else {
+          *reinterpret_cast<float4*>(slot + (size_t)rr * DH + ch) = a;
+          if (ch == 0) {
+            slot[R * DH + rr] = M;
+            slot[R * DH + R + rr] = L;
           }
         }
-        __syncthreads();
       }
+      __syncthreads();  // the buffer is free again
     }
     if (!whole) {
-      if (tid < rows) {
-        float M = -INFINITY, L = 0.f;
-        for (int w = 0; w < kSplitW; ++w) M = fmaxf(M, s_m[w][tid]);
-        for (int w = 0; w < kSplitW; ++w) L += s_m[w][tid] == -INFINITY ? 0.f : s_l[w][tid] * ex2(s_m[w][tid] - M);
-        slot[R * DH + tid] = M;
-        slot[R * DH + R + tid] = L;
-      }
       // the tile's parts lie with teams ta .. tb, the first of which names its counter
-      const unsigned len = cons.s.c1 - cons.s.c0;
-      const int ta = team_of(C, nc, cons.at), tb = team_of(C, nc, cons.at + len - 1), parts = tb - ta + 1;
+      const int ta = team_of(C, nc, w.at + p.tile_cost), tb = team_of(C, nc, w.at + w.len(p) - 1), parts = tb - ta + 1;
+      bool last;
       __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        s_last = atomicAdd(p.counters + ta, 1u) == (unsigned)(parts - 1);
-        if (s_last) p.counters[ta] = 0;
+      if constexpr (WARPS) {
+        __syncwarp();
+        unsigned old = 0;
+        if (lane == 0) {
+          old = atomicAdd(p.counters + ta, 1u);
+          if (old == (unsigned)(parts - 1)) p.counters[ta] = 0;
+        }
+        last = __shfl_sync(0xffffffffu, old, 0) == (unsigned)(parts - 1);
+      } else {
+        __syncthreads();
+        if (tid == 0) {
+          s_last = atomicAdd(p.counters + ta, 1u) == (unsigned)(parts - 1);
+          if (s_last) p.counters[ta] = 0;
+        }
+        __syncthreads();
+        last = s_last;
       }
-      __syncthreads();
-      if (s_last) {
+      if (last) {
         __threadfence();
         // team ta's part is the last of its line (slot 1), the others' the first of theirs
         auto part_of = [&](int i) { return p.slots + (size_t)(2 * (ta + i) + (i == 0 ? 1 : 0)) * p.slot_floats; };
-        for (int i = tid; i < rows * DH / 4; i += kSplitT) {
+        for (int i = WARPS ? lane : tid; i < rows * DH / 4; i += 32 * TEAM) {
           const int rr = i / (DH / 4), ch = (i % (DH / 4)) * 4;
           float M = -INFINITY;
+#pragma unroll 4
           for (int k = 0; k < parts; ++k) M = fmaxf(M, __ldcg(part_of(k) + R * DH + rr));
           float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
           float L = 0.f;
+#pragma unroll 4
           for (int k = 0; k < parts; ++k) {
             const float* q = part_of(k);
-            const float mk = __ldcg(q + R * DH + rr), w = mk == -INFINITY ? 0.f : ex2(mk - M);
+            const float mk = __ldcg(q + R * DH + rr), f = mk == -INFINITY ? 0.f : ex2(mk - M);
             const float4 x = __ldcg(reinterpret_cast<const float4*>(q + (size_t)rr * DH + ch));
-            L += __ldcg(q + R * DH + R + rr) * w;
-            a.x += x.x * w;
-            a.y += x.y * w;
-            a.z += x.z * w;
-            a.w += x.w * w;
+            L += __ldcg(q + R * DH + R + rr) * f;
+            a.x += x.x * f;
+            a.y += x.y * f;
+            a.z += x.z * f;
+            a.w += x.w * f;
           }
-          const float inv = L == 0.f ? 0.f : 1.f / L;
-          const int qr = cons.tile * R + rr;
-          const int64_t at = ((int64_t)(cons.r.q0 + qr / p.G) * p.Hq + cons.hk * p.G + qr % p.G) * DH + ch;
-          if constexpr (BF16) {
-            const __nv_bfloat162 x = __floats2bfloat162_rn(a.x * inv, a.y * inv), y = __floats2bfloat162_rn(a.z * inv, a.w * inv);
-            *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + at) =
-                make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-          } else {
-            *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at) =
-                make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-          }
+          store_row<BF16>(p, w.r, w.hk, w.tile * R + rr, ch, a, L);
         }
       }
     }
-    if (cons.at + (unsigned)(cons.s.c1 - cons.s.c0) >= u1) break;
-    cons.next(p, pre);
-    __syncthreads();  // s_m, s_l and the merge buffer are free again
+    if (w.at + w.len(p) >= u1) break;
+    w.next(p);
   }
-  cp_wait<0>();
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // ------------------------------------------------------------------------------------
@@ -804,34 +882,49 @@ static int split_rows(int64_t dh, int64_t rows) { return rows <= 8 || dh == 256 
 static size_t split_slot_floats(int64_t dh, int64_t rows) { return (size_t)split_rows(dh, rows) * (dh + 2); }
 
 size_t kv8_attention_ws_size(int64_t dh, int64_t rows) {
-  return round_up((size_t)kGridCap * 4, kAlign) + round_up((size_t)2 * kGridCap * split_slot_floats(dh, rows) * 4, kAlign);
+  return round_up((size_t)kMaxTeams * 4, kAlign) + round_up((size_t)2 * kMaxTeams * split_slot_floats(dh, rows) * 4, kAlign);
+}
+
+using SplitKernel = void (*)(const AttnParams);
+struct SplitPick {
+  SplitKernel kern;
+  int threads;
+  size_t smem;
+};
+
+template <bool BF16, bool E4M3, int DH, int NT>
+static SplitPick split_pick(bool warps) {
+  using Sh = SplitShape<BF16, DH, NT>;
+  return {warps ? k_kv8_attn_split<BF16, E4M3, DH, NT, true> : k_kv8_attn_split<BF16, E4M3, DH, NT, false>, Sh::THREADS, Sh::SMEM};
 }
 
 template <bool BF16, bool E4M3>
-static void (*split_kernel(int64_t dh, int rows))(AttnParams) {
-  if (dh == 64) return rows == 8 ? k_kv8_attn_split<BF16, E4M3, 64, 1> : k_kv8_attn_split<BF16, E4M3, 64, 2>;
-  if (dh == 128) return rows == 8 ? k_kv8_attn_split<BF16, E4M3, 128, 1> : k_kv8_attn_split<BF16, E4M3, 128, 2>;
-  return k_kv8_attn_split<BF16, E4M3, 256, 1>;
+static SplitPick split_pick(int64_t dh, int rows, bool warps) {
+  if (dh == 64) return rows == 8 ? split_pick<BF16, E4M3, 64, 1>(warps) : split_pick<BF16, E4M3, 64, 2>(warps);
+  if (dh == 128) return rows == 8 ? split_pick<BF16, E4M3, 128, 1>(warps) : split_pick<BF16, E4M3, 128, 2>(warps);
+  return split_pick<BF16, E4M3, 256, 1>(warps);
 }
 
 static wina_status_t launch_split(AttnParams& p, bool bf16, int64_t rows, cudaStream_t s) {
   const int64_t dh = p.c.dh;
   const int R = split_rows(dh, rows);
-  const size_t stage = (size_t)2 * (dh == 256 ? 16 : 32) * dh * kSplitW, pre = round_up((size_t)(p.B + 1) * 4, 16);
-  // three chunks a warp, or two where a very large batch's prefix sums need the room
-  p.stages = 3;
-  size_t smem = 3 * stage + kMergeBytes + pre;
-  if (smem > (size_t)222 * 1024) {
-    p.stages = 2;
-    smem -= stage;
-  }
   p.slot_floats = (int)split_slot_floats(dh, rows);
-  const bool e4 = p.c.format == KV8_E4M3;
-  void (*kern)(AttnParams) = bf16 ? (e4 ? split_kernel<true, true>(dh, R) : split_kernel<true, false>(dh, R))
-                                  : (e4 ? split_kernel<false, true>(dh, R) : split_kernel<false, false>(dh, R));
   const int sms = device_sm_count();
   if (sms < 1) return WINA_ERR_CUDA;
-  return cuda_status(launch_kernel(kern, dim3((unsigned)std::min(sms, kGridCap)), dim3(kSplitT), smem, s, false, p));
+  const int64_t tiles = p.B * p.c.heads * ((rows + R - 1) / R);
+  p.tiles = (int)std::min<int64_t>(tiles, INT32_MAX);
+  // Two tiles or more to an SM: each warp works for itself, so that the tiles' fixed costs (4 us:
+  // queries, one dependent pass, joining) run side by side; fewer: a CTA's warps share a tile.
+  // Measured (32 / 8 heads of 128): 512 tiles of 10 K keys 219 us against 232 us by CTAs, 2064
+  // tiles of 100 keys 42 against 98; 128 tiles of 9 K keys 72 us against 63, 8 of 16 K 149
+  // against 22.
+  const bool warps = tiles >= 2 * sms;
+  p.tile_cost = warps ? 2 : tiles * 2 <= sms ? 0 : 16;
+  const bool e4 = p.c.format == KV8_E4M3;
+  const SplitPick k = bf16 ? (e4 ? split_pick<true, true>(dh, R, warps) : split_pick<true, false>(dh, R, warps))
+                           : (e4 ? split_pick<false, true>(dh, R, warps) : split_pick<false, false>(dh, R, warps));
+  const size_t smem = k.smem + round_up((size_t)pre_entries(p.B) * 4, 16);
+  return cuda_status(launch_kernel(k.kern, dim3((unsigned)std::min(sms, kMaxCtas)), dim3((unsigned)k.threads), smem, s, false, p));
 }
 
 }  // namespace wina
@@ -878,6 +971,6 @@ extern "C" wina_status_t kv8_attention(const kv8_cache_t* cache, const void* q, 
   p.out = out;
   p.status = status_dev;
   p.counters = reinterpret_cast<uint32_t*>(ws);
-  p.slots = reinterpret_cast<float*>((char*)ws + round_up((size_t)kGridCap * 4, kAlign));
+  p.slots = reinterpret_cast<float*>((char*)ws + round_up((size_t)kMaxTeams * 4, kAlign));
   return launch_split(p, qdt == WINA_BF16, max_q * (Hq / cache->heads), (cudaStream_t)stream);
 }
