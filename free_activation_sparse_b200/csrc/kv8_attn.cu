@@ -11,234 +11,9 @@
 #include <algorithm>
 #include <cmath>
 
-#include "internal.h"
-#include "kv8.cuh"
-#include "tc.cuh"
+#include "kv8_attn.cuh"
 
 namespace wina {
-
-using namespace kv8;
-
-constexpr float kLog2e = 1.4426950408889634f;
-
-struct AttnParams {
-  kv8_cache_t c;
-  const void* q;
-  int64_t ld_q;
-  int T, Hq, G, shift;
-  const int32_t* table;
-  int width;
-  const int32_t* kv_len;
-  const int32_t* cu_q;
-  int B, max_q;
-  float scale, softcap;
-  int window;
-  void* out;
-  int32_t* status;
-  uint32_t* counters;  // [kMaxTeams], zero between calls
-  float* slots;        // [2 * kMaxTeams][slot_floats]
-  int slot_floats;
-  int tiles;      // tiles of query rows, over all heads, at most
-  int tile_cost;  // a tile's fixed cost, in chunks
-};
-
-// ------------------------------------------------------------------------------------
-// the work: tiles of query rows, chunks of keys
-// ------------------------------------------------------------------------------------
-
-// A request's queries and keys, clamped to what the tables hold.
-struct Req {
-  int q0, n, nq, kv;  // first row, queries, queries written (at most max_q), keys
-};
-
-__device__ __forceinline__ Req load_req(const AttnParams& p, int b) {
-  Req r;
-  if (p.cu_q) {
-    const int a = __ldg(p.cu_q + b), e = __ldg(p.cu_q + b + 1);
-    r.q0 = max(0, min(a, p.T));
-    r.n = max(0, min(e, p.T) - r.q0);
-  } else {
-    r.q0 = b;
-    r.n = 1;
-  }
-  r.nq = min(r.n, p.max_q);
-  const int room = p.width << p.shift;
-  r.kv = max(0, min(__ldg(p.kv_len + b), room));
-  return r;
-}
-
-// Whether load_req had to clamp something.
-__device__ __forceinline__ bool bad_req(const AttnParams& p, int b) {
-  bool bad = false;
-  if (p.cu_q) {
-    const int a = __ldg(p.cu_q + b), e = __ldg(p.cu_q + b + 1);
-    bad = a < 0 || e < a || e > p.T || e - a > p.max_q;
-  }
-  const int kv = __ldg(p.kv_len + b), room = p.width << p.shift;
-  return bad || kv < 0 || kv > room;
-}
-
-// The keys [lo, hi) that rows r0 .. r0 + R - 1 of a request see (row = query * G + head in
-// the group), and the chunks of CH keys they lie in. A tile that sees nothing has one chunk
-// with no keys, so that its rows get their zeros on the common path.
-struct Span {
-  int lo, hi, c0, c1;
-};
-
-template <int R, int CH>
-__device__ __forceinline__ Span tile_span(const AttnParams& p, const Req& r, int tile) {
-  const int r0 = tile * R, r1 = min(r0 + R, r.nq * p.G) - 1;
-  Span s;
-  s.hi = r.kv - r.n + r1 / p.G + 1;
-  s.lo = p.window > 0 ? max(0, r.kv - r.n + r0 / p.G - p.window + 1) : 0;
-  if (s.hi <= s.lo) {
-    s.lo = s.hi = s.c0 = 0;
-    s.c1 = 1;
-  } else {
-    s.c0 = s.lo / CH;
-    s.c1 = (s.hi + CH - 1) / CH;
-  }
-  return s;
-}
-
-template <int R>
-__device__ __forceinline__ int tiles_of(const AttnParams& p, const Req& r) {
-  return (r.nq * p.G + R - 1) / R;
-}
-
-// Cost of all of a request's tiles, for one kv head. p.tile_cost is what a tile costs besides
-// its chunks (its queries, the joining of its parts), in chunks; it lies before the tile's
-// first chunk on the line of work.
-template <int R, int CH>
-__device__ __forceinline__ unsigned long long req_cost(const AttnParams& p, const Req& r) {
-  const int nt = tiles_of<R>(p, r);
-  unsigned long long c = 0;
-  for (int t = 0; t < nt; ++t) {
-    const Span s = tile_span<R, CH>(p, r, t);
-    c += s.c1 - s.c0 + p.tile_cost;
-  }
-  return c;
-}
-
-// Prefix sums of req_cost before every fourth request, in shared memory (pre[ceil(B / 4)] the
-// total). Returns false where they pass 32 bits (more than 2^37 keys read: no cache is that
-// large).
-constexpr int kPreStep = 4;
-__host__ __device__ constexpr int pre_entries(int B) { return (B + kPreStep - 1) / kPreStep + 1; }
-
-template <int NTHR, int R, int CH>
-__device__ bool cost_prefix(const AttnParams& p, uint32_t* pre, uint32_t* red) {
-  unsigned long long run = 0;
-  __shared__ int s_over;
-  if (threadIdx.x == 0) s_over = 0;
-  __syncthreads();
-  for (int b0 = 0; b0 < p.B; b0 += NTHR) {
-    const int b = b0 + threadIdx.x;
-    unsigned long long c = 0;
-    if (b < p.B) {
-      c = req_cost<R, CH>(p, load_req(p, b));
-      if (blockIdx.x == 0 && bad_req(p, b)) record_status(p.status, WINA_ERR_INVALID_ARG);
-    }
-    if (c > 0xffffffffu / NTHR) s_over = 1;  // then the block's sum fits 32 bits below
-    uint32_t total;
-    const uint32_t ex = block_excl_scan<NTHR>((uint32_t)min(c, (unsigned long long)(0xffffffffu / NTHR)), red, &total);
-    if (b < p.B && b % kPreStep == 0) pre[b / kPreStep] = (uint32_t)run + ex;
-    run += total;
-    if (run > 0xffffffffu) s_over = 1;
-  }
-  if (threadIdx.x == 0) pre[pre_entries(p.B) - 1] = (uint32_t)run;
-  __syncthreads();
-  return s_over == 0;
-}
-
-// A walk over tiles: requests in order, in each the kv heads, in each the row tiles.
-template <int R, int CH>
-struct Walk {
-  int b, hk, tile, nt;
-  Req r;
-  Span s;
-  unsigned long long at;  // the line's units before this tile
-
-  __device__ __forceinline__ unsigned len(const AttnParams& p) const { return (unsigned)(s.c1 - s.c0 + p.tile_cost); }
-
-  // the tile that holds unit u
-  __device__ __forceinline__ void locate(const AttnParams& p, const uint32_t* pre, unsigned long long u) {
-    int lo = 0, hi = pre_entries(p.B) - 1;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if ((unsigned long long)pre[mid] * p.c.heads <= u) lo = mid;
-      else hi = mid;
-    }
-    b = lo * kPreStep;
-    unsigned long long rem = u - (unsigned long long)pre[lo] * p.c.heads, cost;
-    for (;; ++b) {
-      r = load_req(p, b);
-      cost = req_cost<R, CH>(p, r);
-      if (rem < cost * p.c.heads) break;
-      rem -= cost * p.c.heads;
-    }
-    nt = tiles_of<R>(p, r);
-    hk = (int)(rem / cost);
-    unsigned in = (unsigned)(rem - (unsigned long long)hk * cost);
-    tile = 0;
-    s = tile_span<R, CH>(p, r, 0);
-    while (in >= len(p)) {
-      in -= len(p);
-      s = tile_span<R, CH>(p, r, ++tile);
-    }
-    at = u - in;
-  }
-  // to the next tile (there is one)
-  __device__ __forceinline__ void next(const AttnParams& p) {
-    at += len(p);
-    if (++tile == nt) {
-      tile = 0;
-      if (++hk == (int)p.c.heads) {
-        hk = 0;
-        do r = load_req(p, ++b);
-        while (r.nq == 0 && b < p.B - 1);
-        nt = tiles_of<R>(p, r);
-      }
-    }
-    s = tile_span<R, CH>(p, r, tile);
-  }
-};
-
-// The line's [0, C) units over nc teams: team i has [C i / nc, C (i + 1) / nc); the team that
-// has unit u.
-__device__ __forceinline__ unsigned long long team_start(unsigned long long C, int nc, int i) { return C * i / nc; }
-__device__ __forceinline__ int team_of(unsigned long long C, int nc, unsigned long long u) {
-  return (int)(((u + 1) * nc - 1) / C);
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// The two low (high) bytes of w as float16 numbers. Exact: int8 through 1024 + (byte + 128),
-// whose float16 step is 1 (the word already xor-ed by biased()); e4m3 is a subset of float16.
-template <bool E4M3, bool HIGH>
-__device__ __forceinline__ uint32_t half2_of(uint32_t w) {
-  if constexpr (E4M3) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(HIGH ? w >> 16 : w & 0xffffu), __NV_E4M3);
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
-  } else {
-    const uint32_t u = __byte_perm(w, 0x64646464u, HIGH ? 0x4342 : 0x4140);
-    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(0x6480)));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  }
-}
-template <bool E4M3>
-__device__ __forceinline__ uint32_t biased(uint32_t w) {
-  return E4M3 ? w : w ^ 0x80808080u;
-}
-
-__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 
 // 16 bytes to shared memory, of which `bytes` are read and the rest zero, under an L2 policy.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes, uint64_t pol) {
@@ -254,7 +29,6 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int byt
 // k_kv8_attn_split
 // ------------------------------------------------------------------------------------
 
-constexpr int kMaxCtas = 160;               // CTAs, one per SM, at most
 constexpr int kMaxWarps = 12;               // consumer warps of a CTA, at most
 constexpr int kMaxTeams = kMaxCtas * kMaxWarps;
 constexpr int kMaxStages = 4;
@@ -282,20 +56,6 @@ template <int DH>
 __device__ __forceinline__ uint32_t staged(int r, int c) {
   if constexpr (DH == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
   else return (c >> 3) * 2048 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-}
-
-// Four channels of a query row (row = query * G + head in the group): sums over weights.
-template <bool BF16>
-__device__ __forceinline__ void store_row(const AttnParams& p, const Req& r, int hk, int row, int ch, float4 a, float L) {
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  const int64_t at = ((int64_t)(r.q0 + row / p.G) * p.Hq + hk * p.G + row % p.G) * p.c.dh + ch;
-  if constexpr (BF16) {
-    const __nv_bfloat162 x = __floats2bfloat162_rn(a.x * inv, a.y * inv), y = __floats2bfloat162_rn(a.z * inv, a.w * inv);
-    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + at) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-  } else {
-    *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-  }
 }
 
 // The variants' sizes. The registers set the number of consumer warps (a tile's sums and
@@ -882,7 +642,9 @@ static int split_rows(int64_t dh, int64_t rows) { return rows <= 8 || dh == 256 
 static size_t split_slot_floats(int64_t dh, int64_t rows) { return (size_t)split_rows(dh, rows) * (dh + 2); }
 
 size_t kv8_attention_ws_size(int64_t dh, int64_t rows) {
-  return round_up((size_t)kMaxTeams * 4, kAlign) + round_up((size_t)2 * kMaxTeams * split_slot_floats(dh, rows) * 4, kAlign);
+  size_t slots = (size_t)2 * kMaxTeams * split_slot_floats(dh, rows);
+  if (prompt_takes(true, dh, rows)) slots = std::max(slots, (size_t)2 * kMaxCtas * prompt_slot_floats(dh));
+  return round_up((size_t)kMaxTeams * 4, kAlign) + round_up(slots * 4, kAlign);
 }
 
 using SplitKernel = void (*)(const AttnParams);
@@ -972,5 +734,7 @@ extern "C" wina_status_t kv8_attention(const kv8_cache_t* cache, const void* q, 
   p.status = status_dev;
   p.counters = reinterpret_cast<uint32_t*>(ws);
   p.slots = reinterpret_cast<float*>((char*)ws + round_up((size_t)kMaxTeams * 4, kAlign));
-  return launch_split(p, qdt == WINA_BF16, max_q * (Hq / cache->heads), (cudaStream_t)stream);
+  const int64_t rows = max_q * (Hq / cache->heads);
+  if (prompt_takes(qdt == WINA_BF16, cache->dh, rows)) return launch_prompt(p, rows, (cudaStream_t)stream);
+  return launch_split(p, qdt == WINA_BF16, rows, (cudaStream_t)stream);
 }
