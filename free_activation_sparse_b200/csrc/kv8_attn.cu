@@ -337,8 +337,9 @@ __global__ void __launch_bounds__(SplitShape<BF16, DH, NT>::THREADS, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const uint32_t a = biased<E4M3>(xs[k]), b = biased<E4M3>(ys[k]);
-            const uint32_t fr[4] = {half2_of<E4M3, false>(a), half2_of<E4M3, false>(b), half2_of<E4M3, true>(a),
-                                    half2_of<E4M3, true>(b)};
+            uint32_t fr[4];
+            half4_of<E4M3>(a, fr[0], fr[2]);
+            half4_of<E4M3>(b, fr[1], fr[3]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -473,8 +474,9 @@ __global__ void __launch_bounds__(SplitShape<BF16, DH, NT>::THREADS, 1)
             for (int e = 0; e < 2; ++e) {
               const uint32_t a = __byte_perm(x[0][q], x[1][q], e ? 0x7362 : 0x5140);
               const uint32_t b = __byte_perm(x[2][q], x[3][q], e ? 0x7362 : 0x5140);
-              const uint32_t fr[4] = {half2_of<E4M3, false>(a), half2_of<E4M3, true>(a), half2_of<E4M3, false>(b),
-                                      half2_of<E4M3, true>(b)};
+              uint32_t fr[4];
+              half4_of<E4M3>(a, fr[0], fr[1]);
+              half4_of<E4M3>(b, fr[2], fr[3]);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

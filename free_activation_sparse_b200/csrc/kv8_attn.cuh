@@ -208,17 +208,20 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// The two low (high) bytes of w as float16 numbers. Exact: int8 through 1024 + (byte + 128),
+// The four bytes of w as float16 numbers, two to a word. Exact: int8 through 1024 + (byte + 128),
 // whose float16 step is 1 (the word already xor-ed by biased()); e4m3 is a subset of float16.
-template <bool E4M3, bool HIGH>
-__device__ __forceinline__ uint32_t half2_of(uint32_t w) {
+template <bool E4M3>
+__device__ __forceinline__ void half4_of(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if constexpr (E4M3) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(HIGH ? w >> 16 : w & 0xffffu), __NV_E4M3);
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
   } else {
-    const uint32_t u = __byte_perm(w, 0x64646464u, HIGH ? 0x4342 : 0x4140);
-    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(0x6480)));
-    return *reinterpret_cast<const uint32_t*>(&r);
+    const uint32_t u = __byte_perm(w, 0x64646464u, 0x4140), v = __byte_perm(w, 0x64646464u, 0x4342);
+    const __half2 z = __half2half2(__ushort_as_half(0x6480));
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&u), z), y = __hsub2(*reinterpret_cast<const __half2*>(&v), z);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
   }
 }
 template <bool E4M3>

@@ -17,8 +17,11 @@ namespace {
 
 constexpr int kRows = 256;        // query rows of a tile: two halves of 128
 constexpr int kKeys = 128;        // keys of a chunk
-constexpr int kThreads = 416;     // warps 0-3, 4-7: softmax of a half; 8-11: bytes; 12: matrix products
+constexpr int kThreads = 640;     // warps 0-3, 4-7: softmax of a half; 8-15: bytes; 16: matrix products
 constexpr int kInfo = 4;          // chunks whose factors are kept
+// Registers a thread, of the 96 (640 threads) that it is launched with.
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 136, kByteRegs = 80, kMmaRegs = 40;
+static_assert(256 * kSoftmaxRegs + 256 * kByteRegs + 128 * kMmaRegs <= kThreads * kLaunchRegs, "register split");
 constexpr float kOffLog2 = 7.f;   // weights are held times 2^7 ...
 constexpr float kLazyLog2 = 8.f;  // ... and may outgrow the reference maximum by 2^8 before O is rescaled
 constexpr float kByteUp = 8.f;    // bytes are held times 8 scale / reference, the reference kept
@@ -92,13 +95,36 @@ __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.a
 // of 64 numbers, 128 bytes a row, 128-byte swizzle.
 __device__ __forceinline__ uint32_t operand_at(int r, int c) { return (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4); }
 
-// Two bytes as float16 numbers times f (two alike): exact where f is a power of two and the
+// Four bytes as float16 numbers times f (two alike): exact where f is a power of two and the
 // result no subnormal number.
-template <bool E4M3, bool HIGH>
-__device__ __forceinline__ uint32_t scaled_half2(uint32_t w, __half2 f) {
-  const uint32_t x = half2_of<E4M3, HIGH>(w);
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), f);
-  return *reinterpret_cast<const uint32_t*>(&r);
+template <bool E4M3>
+__device__ __forceinline__ uint2 scaled_half4(uint32_t w, __half2 f) {
+  uint32_t lo, hi;
+  half4_of<E4M3>(biased<E4M3>(w), lo, hi);
+  const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&lo), f), y = __hmul2(*reinterpret_cast<const __half2*>(&hi), f);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+}
+
+// Two float32 numbers at a time: a * b + c, a + b; the larger of three.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 }  // namespace
@@ -107,11 +133,11 @@ __device__ __forceinline__ uint32_t scaled_half2(uint32_t w, __half2 f) {
 // and kv head, row = query * G + head of the group, times chunks of 128 keys), joined like the
 // parts of k_kv8_attn_split. Two halves of 128 rows take turns: while one's softmax runs, the
 // tensor cores work for the other.
-//   warps 8-11 (bytes): a chunk's keys and values from the pages into shared memory as float16
+//   warps 8-15 (bytes): a chunk's keys and values from the pages into shared memory as float16
 //     times 8 scale / reference, the reference being the first chunk's largest scale, raised
 //     when a scale passes 16 times it: exact for power-of-two scales over 2^17 of range, so a
 //     score needs one factor per row and chunk and a weight none. Loads run a chunk ahead.
-//   warp 12: S = Q K^T of either half as soon as its last P has been used, O += P V as soon as P
+//   warp 16: S = Q K^T of either half as soon as its last P has been used, O += P V as soon as P
 //     is there (P is the A operand from tensor memory, in the place of S).
 //   warps 0-3, 4-7 (softmax, a thread per row): the row's maximum in one pass over S, the
 //     weights as float16 in a second; O is rescaled only when a maximum outgrows its
@@ -137,8 +163,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
   uint32_t* pre = reinterpret_cast<uint32_t*>(vs + 2 * TILE);
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&k_full[i], 128u);
-      tc::mbar_init(&v_full[i], 128u);
+      tc::mbar_init(&k_full[i], 256u);
+      tc::mbar_init(&v_full[i], 256u);
       tc::mbar_init(&k_empty[i], 1u);
       tc::mbar_init(&v_empty[i], 1u);
       tc::mbar_init(&s_full[i], 1u);
@@ -158,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
   }
   const int nc = (int)min((unsigned long long)gridDim.x, C), team = blockIdx.x;  // every team has a unit
   if (team >= nc) return;
-  if (warp == 12) tc::tmem_alloc(&s_taddr, 512u);
+  if (warp == 16) tc::tmem_alloc(&s_taddr, 512u);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -181,53 +207,49 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
     }
   };
   W w;
-  w.locate(p, pre, u0);
 
-  if (warp >= 8 && warp < 12) {
+  if (warp >= 8 && warp < 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kByteRegs));
+    w.locate(p, pre, u0);
     // ---------------- bytes ----------------
+    // warp 8 + d has 16-key group d of every chunk: one run of a page
     constexpr int PPR = DH / 16;         // 16-byte pieces of a row of bytes
     constexpr int RPI = 32 / PPR;        // rows of a warp's load
-    constexpr int N = 32 / RPI;          // loads of a warp's 32 keys
-    const int wk = (warp - 8) * 32;      // this warp's keys of a chunk
-    const int lr = lane / PPR, lc = lane % PPR;
+    constexpr int N = 16 / RPI;          // loads of 16 keys
+    const int d = warp - 8, lr = lane / PPR, lc = lane % PPR;
     const int page_mask = (1 << p.shift) - 1;
     uint4 kr[N], vr[N];
-    // loads of one side of a chunk; head: (page, head) of its 16-key group `lane`, -1 where none
+    // loads of one side of this warp's group; head: its (page, head), -1 where there is none
     auto load = [&](int64_t head, int key0, int lo, int hi, const void* base, uint4 (&r)[N]) {
+      const int key = key0 + 16 * d;
+      const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(base) +
+                                                        ((head << p.shift) + (key & page_mask)) * DH) + lane;
+      const bool all = head >= 0 && key >= lo && key + 16 <= hi;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const int row = wk + i * RPI + lr, key = key0 + row;
-        const int64_t h = __shfl_sync(0xffffffffu, head, (wk + i * RPI) / 16);
+        const int k = key + i * RPI + lr;
         r[i] = make_uint4(0, 0, 0, 0);
-        if (h >= 0 && key >= lo && key < hi)
-          r[i] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(base) + ((h << p.shift) + (key & page_mask)) * DH + lc * 16));
+        if (all || (head >= 0 && k >= lo && k < hi)) r[i] = __ldg(src + 32 * i);
       }
     };
-    // one side into its tile; f: the factor of 16-key group lane
+    // One side into its tile, times f. The lanes of a row's second half store their pieces in the
+    // other order, so that a row's eight lanes fall on different banks. (Places without a byte
+    // were loaded as 0, which either format shows as 0.)
+    const bool swap = lc & 4;
+    const int c0 = 2 * lc + (swap ? 1 : 0), c1 = 2 * lc + (swap ? 0 : 1);
+    const uint32_t at0 = operand_at(16 * d + lr, c0), at1 = operand_at(16 * d + lr, c1);
     auto store = [&](const uint4 (&r)[N], unsigned char* tile, float f) {
+      const __half2 m = __float2half2_rn(f);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const int row = wk + i * RPI + lr;
-        const __half2 m = __float2half2_rn(__shfl_sync(0xffffffffu, f, (wk + i * RPI) / 16));
-        const uint32_t u[4] = {biased<E4M3>(r[i].x), biased<E4M3>(r[i].y), biased<E4M3>(r[i].z), biased<E4M3>(r[i].w)};
-        uint4 a, b;
-        a.x = scaled_half2<E4M3, false>(u[0], m);
-        a.y = scaled_half2<E4M3, true>(u[0], m);
-        a.z = scaled_half2<E4M3, false>(u[1], m);
-        a.w = scaled_half2<E4M3, true>(u[1], m);
-        b.x = scaled_half2<E4M3, false>(u[2], m);
-        b.y = scaled_half2<E4M3, true>(u[2], m);
-        b.z = scaled_half2<E4M3, false>(u[3], m);
-        b.w = scaled_half2<E4M3, true>(u[3], m);
-        // the lanes of a row's second half store their pieces in the other order, so that a
-        // row's eight lanes fall on different banks
-        const bool swap = lc & 4;
-        *reinterpret_cast<uint4*>(tile + operand_at(row, 2 * lc + (swap ? 1 : 0))) = swap ? b : a;
-        *reinterpret_cast<uint4*>(tile + operand_at(row, 2 * lc + (swap ? 0 : 1))) = swap ? a : b;
+        // row i * RPI further on: 128 bytes a row, and another permutation where RPI is 4
+        const uint32_t flip = RPI == 4 && (i & 1) ? 64u : 0u;
+        const uint2 a = scaled_half4<E4M3>(swap ? r[i].z : r[i].x, m), b = scaled_half4<E4M3>(swap ? r[i].w : r[i].y, m);
+        *reinterpret_cast<uint4*>(tile + (at0 ^ flip) + i * RPI * 128) = make_uint4(a.x, a.y, b.x, b.y);
+        const uint2 e = scaled_half4<E4M3>(swap ? r[i].x : r[i].z, m), g = scaled_half4<E4M3>(swap ? r[i].y : r[i].w, m);
+        *reinterpret_cast<uint4*>(tile + (at1 ^ flip) + i * RPI * 128) = make_uint4(e.x, e.y, g.x, g.y);
       }
     };
-    // Places without a byte were loaded as 0, which the int8 form shows as 0 too: 0 ^ 0x80 is
-    // 128, from which 128 is taken.
     int c, to;
     part(w, c, to);
     // The chunk at or after c in the walk, with the page indices of its groups (lanes 0-7) on
@@ -259,7 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
       ++c;
       return n;
     };
-    auto head_of = [&](const Next& n) { return n.pg >= 0 && n.pg < p.c.n_pages ? (int64_t)n.pg * p.c.heads + n.hk : (int64_t)-1; };
+    auto head_of = [&](const Next& n) {  // of group `lane`
+      return n.pg >= 0 && n.pg < p.c.n_pages ? (int64_t)n.pg * p.c.heads + n.hk : (int64_t)-1; };
     // chunk `it` is stored while chunk it + 1 is loaded and the pages of chunk it + 2 are found
     Next n = seek();
     bool any = n.any;
@@ -268,8 +291,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
     uint32_t bad = __ballot_sync(0xffffffffu, any && n.used && head < 0);
     float kscale = 0.f, vscale = 0.f, kref = 0.f, sref = 0.f;
     if (any) {
-      load(head, n.key0, n.lo, n.hi, p.c.k, kr);
-      load(head, n.key0, n.lo, n.hi, p.c.v, vr);
+      const int64_t mine = __shfl_sync(0xffffffffu, head, d);
+      load(mine, n.key0, n.lo, n.hi, p.c.k, kr);
+      load(mine, n.key0, n.lo, n.hi, p.c.v, vr);
       if (head >= 0) {
         kscale = __ldg(p.c.k_scale + head);
         vscale = __ldg(p.c.v_scale + head);
@@ -297,7 +321,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
       vm = __shfl_sync(0xffffffffu, vm, 0);
       if (km > kGrow * kref || kref == 0.f) kref = fmaxf(km, 1.17549435e-38f);
       if (vm > kGrow * sref || sref == 0.f) sref = fmaxf(vm, 1.17549435e-38f);
-      const float kf = lost ? __uint_as_float(0x7fc00000u) : kByteUp * (kscale / kref), vf = lost ? 0.f : kByteUp * (vscale / sref);
+      float kf = lost ? __uint_as_float(0x7fc00000u) : kByteUp * (kscale / kref), vf = lost ? 0.f : kByteUp * (vscale / sref);
+      kf = __shfl_sync(0xffffffffu, kf, d);
+      vf = __shfl_sync(0xffffffffu, vf, d);
       // keys
       if (it >= 2) wait(&k_empty[st], (uint32_t)((it / 2 - 1) & 1));
       if (tid == 8 * 32) {
@@ -309,10 +335,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
       fence_async_smem();
       tc::mbar_arrive(&k_full[st]);
       any = n.any;
+      int64_t mine = -1;
       if (any) {
         head = head_of(n);
         at = n.at;
-        load(head, n.key0, n.lo, n.hi, p.c.k, kr);
+        mine = __shfl_sync(0xffffffffu, head, d);
+        load(mine, n.key0, n.lo, n.hi, p.c.k, kr);
       }
       // values
       if (it >= 2) wait(&v_empty[st], (uint32_t)((it / 2 - 1) & 1));
@@ -320,16 +348,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
       fence_async_smem();
       tc::mbar_arrive(&v_full[st]);
       if (any) {
-        load(head, n.key0, n.lo, n.hi, p.c.v, vr);
+        load(mine, n.key0, n.lo, n.hi, p.c.v, vr);
         kscale = head >= 0 ? __ldg(p.c.k_scale + head) : 0.f;
         vscale = head >= 0 ? __ldg(p.c.v_scale + head) : 0.f;
         bad = __ballot_sync(0xffffffffu, n.used && head < 0);
         n = seek();
       }
     }
-  } else if (warp == 12) {
+  } else if (warp >= 16) {
     // ---------------- matrix products (one thread) ----------------
-    if (lane == 0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+    if (warp == 16 && lane == 0) {
+      w.locate(p, pre, u0);
       const uint32_t id_qk = idesc_f16(kKeys, 0), id_pv = idesc_f16(DH, 1);
       int it = 0, tiles = 0, halves1 = 0, pn[2] = {0, 0};
       auto qk = [&](int h, int st) {
@@ -383,6 +413,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
     }
   } else {
     // ---------------- softmax: half h, a thread per row ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    w.locate(p, pre, u0);
     const int h = warp >> 2, lrow = tid & 127;
     const uint32_t tm = taddr + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t ts = tm + h * 128u, to_ = tm + Sh::O_COL + h * 128u;
@@ -450,9 +482,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
               }
             }
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              x0 = fmaxf(x0, __uint_as_float(v[e]));
-              x1 = fmaxf(x1, __uint_as_float(v[e + 1]));
+            for (int e = 0; e < 32; e += 4) {
+              x0 = max3(x0, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+              x1 = max3(x1, __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
             }
           };
           tmem_ld32(ts, a);
@@ -492,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
             sref = info.sref;
           }
           const float mb = m == -INFINITY ? 0.f : m - kOffLog2;
-          float l0 = 0.f, l1 = 0.f;
+          float2 l0 = make_float2(0.f, 0.f), l1 = l0;
           // 32 weights as float16 in the place of scores already read
           auto weigh = [&](uint32_t (&v)[32], int col) {
             uint32_t o[16];
@@ -501,7 +533,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
               for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(tanhf(__uint_as_float(v[e]) * cf) * (p.softcap * kLog2e) - mb);
             } else {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(fmaf(__uint_as_float(v[e]), cf, -mb));
+              for (int e = 0; e < 32; e += 2) {
+                const float2 y = fma2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), make_float2(cf, cf), make_float2(-mb, -mb));
+                v[e] = __float_as_uint(y.x);
+                v[e + 1] = __float_as_uint(y.y);
+              }
             }
             if (masked) {
 #pragma unroll
@@ -512,10 +548,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
             }
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float y = ex2(__uint_as_float(v[e])), z = ex2(__uint_as_float(v[e + 1]));
-              l0 += y;
-              l1 += z;
-              o[e / 2] = pack_half2(y, z);
+              const float2 y = make_float2(ex2(__uint_as_float(v[e])), ex2(__uint_as_float(v[e + 1])));
+              if (e & 2) l1 = add2(l1, y);
+              else l0 = add2(l0, y);
+              o[e / 2] = pack_half2(y.x, y.y);
             }
             tmem_st16(ts + col / 2, o);
           };
@@ -530,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
           weigh(a, 64);
           tc::tmem_ld_wait();
           weigh(b, 96);
-          l += l0 + l1;
+          l += (l0.x + l0.y) + (l1.x + l1.y);
           tmem_st_wait();
           tc::tc_fence_before();
           tc::mbar_arrive(&p_full[h]);
@@ -618,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
   }
   tc::tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 16) {
     tc::tc_fence_after();
     tc::tmem_dealloc(taddr, 512u);
   }
