@@ -121,6 +121,12 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
   return d;
 }
+// tanh x = 1 - 2 / (1 + e^(2 x)), off by at most 2^-22.
+__device__ __forceinline__ float tanh_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(x * (2.f * kLog2e))));
+  return fmaf(-2.f, r, 1.f);
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -361,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
     if (warp == 16 && lane == 0) {
       w.locate(p, pre, u0);
       const uint32_t id_qk = idesc_f16(kKeys, 0), id_pv = idesc_f16(DH, 1);
-      int it = 0, tiles = 0, halves1 = 0, pn[2] = {0, 0};
+      int it = 0, tiles = 0, halves1 = 0, pn = 0, pn1 = 0;
       auto qk = [&](int h, int st) {
         const uint32_t q0 = tc::smem_u32(qs) + h * QTILE, k0 = tc::smem_u32(ks) + st * TILE;
 #pragma unroll
@@ -388,14 +394,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
           halves1 += nh - 1;
           wait(&k_full[it & 1], (uint32_t)((it / 2) & 1));
           tc::tc_fence_after();
+#pragma unroll 1
           for (int h = 0; h < nh; ++h) qk(h, it & 1);
           tc::mma_commit(&k_empty[it & 1]);
           for (int c = from; c < to; ++c, ++it) {
             const int st = it & 1, nst = (it + 1) & 1;
             wait(&v_full[st], (uint32_t)((it / 2) & 1));
             if (c + 1 < to) wait(&k_full[nst], (uint32_t)(((it + 1) / 2) & 1));
+#pragma unroll 1
             for (int h = 0; h < nh; ++h) {
-              wait(&p_full[h], (uint32_t)(pn[h]++ & 1));
+              wait(&p_full[h], (uint32_t)((h ? pn1++ : pn++) & 1));
               tc::tc_fence_after();
               pv(h, st, c == from);
               if (c + 1 < to) qk(h, nst);
@@ -470,38 +478,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
           const int key0 = c * kKeys;
           const bool masked = info.bad || key0 < last_low || key0 + kKeys > first_lim;
           const float cf = fac * info.kfac;
-          uint32_t a[32], b[32];
+          // Both passes are loops of 32 columns, kept short: the three roles' code together has to
+          // stay in the instruction caches (with everything unrolled, warps waited for
+          // instructions a third of the time).
+          uint32_t v[32];
           float x0 = -INFINITY, x1 = -INFINITY;
-          // 32 scores' maximum, places that the row does not see left out
-          auto top = [&](uint32_t (&v)[32], int col) {
-            if (masked) {
+          // places that the row does not see
+          auto leave_out = [&](int col) {
+            const int past = lim - (key0 + col), before = low - (key0 + col);
+            const uint32_t off = info.bad >> (col >> 4);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const int key = key0 + col + e;
-                if (key >= lim || key < low || ((info.bad >> ((col + e) >> 4)) & 1)) v[e] = 0xff800000u;
-              }
-            }
+            for (int e = 0; e < 32; ++e)
+              if (e >= past || e < before || ((off >> (e >> 4)) & 1)) v[e] = 0xff800000u;
+          };
+#pragma unroll 1
+          for (int col = 0; col < kKeys; col += 32) {
+            tmem_ld32(ts + col, v);
+            tc::tmem_ld_wait();
+            if (masked) leave_out(col);
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
               x0 = max3(x0, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
               x1 = max3(x1, __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
             }
-          };
-          tmem_ld32(ts, a);
-          tc::tmem_ld_wait();
-          tmem_ld32(ts + 32, b);
-          top(a, 0);
-          tc::tmem_ld_wait();
-          tmem_ld32(ts + 64, a);
-          top(b, 32);
-          tc::tmem_ld_wait();
-          tmem_ld32(ts + 96, b);
-          top(a, 64);
-          tc::tmem_ld_wait();
-          tmem_ld32(ts, a);  // for the second pass
-          top(b, 96);
+          }
           float x = fmaxf(x0, x1) * cf;
-          if (p.softcap > 0.f) x = tanhf(x) * (p.softcap * kLog2e);
+          if (p.softcap > 0.f) x = tanh_fast(x) * (p.softcap * kLog2e);
           const bool raise = x > m + kLazyLog2 || (m == -INFINITY && x > -INFINITY);
           const float mn = raise ? x : m;
           if (__any_sync(0xffffffffu, raise) || info.sref != sref) {
@@ -509,14 +511,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
             l *= al;
             if (c > from) {
               const float f = al * (sref / info.sref);
-              uint32_t o[32];
 #pragma unroll 1
               for (int j = 0; j < DH; j += 32) {
-                tmem_ld32(to_ + j, o);
+                tmem_ld32(to_ + j, v);
                 tc::tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st32(to_ + j, o);
+                for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+                tmem_st32(to_ + j, v);
               }
               tmem_st_wait();
             }
@@ -525,12 +526,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
           }
           const float mb = m == -INFINITY ? 0.f : m - kOffLog2;
           float2 l0 = make_float2(0.f, 0.f), l1 = l0;
-          // 32 weights as float16 in the place of scores already read
-          auto weigh = [&](uint32_t (&v)[32], int col) {
-            uint32_t o[16];
+          // weights as float16 in the place of scores already read
+#pragma unroll 1
+          for (int col = 0; col < kKeys; col += 32) {
+            tmem_ld32(ts + col, v);
+            tc::tmem_ld_wait();
             if (p.softcap > 0.f) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(tanhf(__uint_as_float(v[e]) * cf) * (p.softcap * kLog2e) - mb);
+              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(tanh_fast(__uint_as_float(v[e]) * cf) * (p.softcap * kLog2e) - mb);
             } else {
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
@@ -539,13 +542,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
                 v[e + 1] = __float_as_uint(y.y);
               }
             }
-            if (masked) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const int key = key0 + col + e;
-                if (key >= lim || key < low || ((info.bad >> ((col + e) >> 4)) & 1)) v[e] = 0xff800000u;
-              }
-            }
+            if (masked) leave_out(col);
+            uint32_t o[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               const float2 y = make_float2(ex2(__uint_as_float(v[e])), ex2(__uint_as_float(v[e + 1])));
@@ -554,18 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
               o[e / 2] = pack_half2(y.x, y.y);
             }
             tmem_st16(ts + col / 2, o);
-          };
-          tc::tmem_ld_wait();
-          tmem_ld32(ts + 32, b);
-          weigh(a, 0);
-          tc::tmem_ld_wait();
-          tmem_ld32(ts + 64, a);
-          weigh(b, 32);
-          tc::tmem_ld_wait();
-          tmem_ld32(ts + 96, b);
-          weigh(a, 64);
-          tc::tmem_ld_wait();
-          weigh(b, 96);
+          }
           l += (l0.x + l0.y) + (l1.x + l1.y);
           tmem_st_wait();
           tc::tc_fence_before();
