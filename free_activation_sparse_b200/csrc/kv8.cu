@@ -111,43 +111,37 @@ __global__ void __launch_bounds__(kPlanT) k_kv8_plan(PlanParams p) {
   const int room = (int)min((long long)p.width << p.shift, 0x7fffffffLL);
   int n_free = *p.n_free;
   if (tid == 0) s_taken = 0;
-  Sum3 run = {0, 0, 0};
-  for (int b0 = 0; b0 < B; b0 += kPlanT) {
-    const int b = b0 + tid;
-    Sum3 v = {0, 0, 0};
-    int sq = 0;
-    if (b < B) {
-      sq = p.seq_len[b];
-      const int nw = p.new_len[b];
-      const bool bad = sq < 0 || sq > room || (nw > 0 && nw > room - sq);
-      const int have = bad ? 0 : (sq + page - 1) >> p.shift;
-      v.a = max(nw, 0);
-      if (!bad) {
-        if (nw < 0) v.c = have;
-        else v.b = (int)(((long long)sq + nw + page - 1) >> p.shift) - have;
-      }
-      if (bad) {
-        sq = ~max(0, min(sq, room));
-        if (blockIdx.x == 0) record_status(p.status, WINA_ERR_INVALID_ARG);
-      }
+  // a thread's consecutive requests, then one scan over the threads
+  const int per = (B + kPlanT - 1) / kPlanT, b_lo = min(tid * per, B), b_hi = min(b_lo + per, B);
+  Sum3 mine = {0, 0, 0};
+#pragma unroll 4
+  for (int b = b_lo; b < b_hi; ++b) {
+    int sq = p.seq_len[b];
+    const int nw = p.new_len[b];
+    const bool bad = sq < 0 || sq > room || (nw > 0 && nw > room - sq);
+    const int have = bad ? 0 : (sq + page - 1) >> p.shift;
+    mine.a += max(nw, 0);
+    if (!bad) {
+      if (nw < 0) mine.c += have;
+      else mine.b += (int)(((long long)sq + nw + page - 1) >> p.shift) - have;
+    } else {
+      sq = ~max(0, min(sq, room));
+      if (blockIdx.x == 0) record_status(p.status, WINA_ERR_INVALID_ARG);
     }
-    Sum3 tot;
-    const Sum3 ex = block_scan3(v, red, &tot);
-    if (b < B) {
-      tok[b] = sat32(run.a + ex.a);
-      need[b] = sat32(run.b + ex.b);
-      back[b] = sat32(run.c + ex.c);
-      seq[b] = sq;
-    }
-    run.a += tot.a;
-    run.b += tot.b;
-    run.c += tot.c;
+    // inclusive within the thread for now
+    tok[b + 1] = sat32(mine.a);
+    need[b + 1] = sat32(mine.b);
+    back[b + 1] = sat32(mine.c);
+    seq[b] = sq;
   }
-  if (tid == 0) {
-    tok[B] = sat32(run.a);
-    need[B] = sat32(run.b);
-    back[B] = sat32(run.c);
+  Sum3 run;
+  const Sum3 ex = block_scan3(mine, red, &run);
+  for (int b = b_lo; b < b_hi; ++b) {
+    tok[b + 1] = sat32(ex.a + tok[b + 1]);
+    need[b + 1] = sat32(ex.b + need[b + 1]);
+    back[b + 1] = sat32(ex.c + back[b + 1]);
   }
+  if (tid == 0) tok[0] = need[0] = back[0] = 0;
   if (n_free < 0 || n_free > p.cells) {
     if (blockIdx.x == 0 && tid == 0) record_status(p.status, WINA_ERR_INVALID_ARG);
     n_free = max(0, min(n_free, p.cells));
@@ -208,7 +202,20 @@ __global__ void __launch_bounds__(kPlanT) k_kv8_plan(PlanParams p) {
       p.table[(int64_t)b * p.width + have + (j - need[b])] = popped_page(j);
     }
   }
-  for (int r = rank * kPlanT + tid; r < pushed; r += ctas * kPlanT) p.free_pages[n_free + r] = pushed_page(r);
+  for (int r0 = rank * kPlanT + tid; r0 < pushed; r0 += 4 * ctas * kPlanT) {
+    // four at a time: their searches and loads do not wait for one another
+    int pg[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = r0 + u * ctas * kPlanT;
+      pg[u] = r < pushed ? pushed_page(r) : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = r0 + u * ctas * kPlanT;
+      if (r < pushed) p.free_pages[n_free + r] = pg[u];
+    }
+  }
   // what may overlay the inputs: after every CTA has read them
   if (ctas > 1) cooperative_groups::this_cluster().sync();
   for (int b = rank * kPlanT + tid; b < B; b += ctas * kPlanT) {
@@ -251,7 +258,9 @@ struct WriteParams {
 // the scale, the bytes. DH / 8 lanes hold a row, eight channels each, so a pass over up to
 // kRows rows has all its 16-byte loads in flight; a run longer than that is read twice, the
 // second time from L1/L2. Bound by HBM for prompts (each element read once, one byte
-// written), by latency for single tokens.
+// written), by latency for single tokens. Four CTAs of 64 registers share an SM: with more rows
+// in registers, or the runs' lengths found beforehand, 15500 bf16 rows of 8 x 128 in pages of 32
+// took 29 to 44 us instead of 25.
 template <bool BF16, bool E4M3, int DH>
 __global__ void __launch_bounds__(32 * kWriteW) k_kv8_write(WriteParams p) {
   constexpr int LPR = DH / 8, RPP = 32 / LPR;  // lanes per row, rows per pass
@@ -310,14 +319,14 @@ __global__ void __launch_bounds__(32 * kWriteW) k_kv8_write(WriteParams p) {
     }
     amax = __reduce_max_sync(0xffffffffu, amax);
     float s;
-    bool void_ = amax >= 0x7f800000u || present != present;  // no scale holds these rows
-    if (void_) {
+    bool lost = amax >= 0x7f800000u || present != present;  // no scale holds these rows
+    if (lost) {
       s = __uint_as_float(0x7fc00000u);
     } else {
       s = pow2_scale<E4M3>(amax);
       if (first && present > s) s = present;
     }
-    if (first && !void_ && s != present) {
+    if (first && !lost && s != present) {
       // the scale grew: the page's older rows, rounded again
       const float f = __fdiv_rn(present, s);
       for (int i = sub; i < first; i += RPP) {
@@ -330,7 +339,7 @@ __global__ void __launch_bounds__(32 * kWriteW) k_kv8_write(WriteParams p) {
         *reinterpret_cast<uint2*>(dst + i * DH) = w;
       }
     }
-    const float inv = void_ ? 0.f : __fdiv_rn(1.f, s);
+    const float inv = lost ? 0.f : __fdiv_rn(1.f, s);
     const bool again = len > IT * RPP;
     for (int i0 = 0; i0 < len; i0 += IT * RPP) {
       if (again) {
@@ -346,7 +355,7 @@ __global__ void __launch_bounds__(32 * kWriteW) k_kv8_write(WriteParams p) {
         if (i < len) {
           float v[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = void_ ? 0.f : r[q].get(e) * inv;
+          for (int e = 0; e < 8; ++e) v[e] = lost ? 0.f : r[q].get(e) * inv;
           const uint2 w = make_uint2(pack4<E4M3>(v[0], v[1], v[2], v[3]), pack4<E4M3>(v[4], v[5], v[6], v[7]));
           *reinterpret_cast<uint2*>(dst + (first + i) * DH) = w;
         }
@@ -354,6 +363,130 @@ __global__ void __launch_bounds__(32 * kWriteW) k_kv8_write(WriteParams p) {
     }
     if (lane == 0 && (first == 0 || s != present)) *scale_at = s;
   }
+}
+
+// The same where a page is more than four times what a warp holds: its longer runs
+// are shared by the CTA's eight warps, which exchange their maxima; the shorter ones are one
+// warp's. (3010 float32 rows of 4 x 256 in pages of 64: 28 us with a warp to an item, 12 us so;
+// with eight warps to each run of 32 bf16 rows of 128, which two hold, 80 us instead of 25.)
+template <bool BF16, bool E4M3, int DH>
+__global__ void __launch_bounds__(32 * kWriteW, 3) k_kv8_write_shared(WriteParams p) {
+  constexpr int LPR = DH / 8, RPP = 32 / LPR;  // lanes per row, rows per pass
+  constexpr int IT = BF16 ? 8 : 4;             // passes held in registers
+  constexpr int ROWS = IT * RPP;               // rows a warp holds
+  __shared__ int s_run[kWriteSeg], s_len[kWriteSeg], s_n;
+  __shared__ uint32_t s_amax[kWriteW];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t0 = blockIdx.x * p.seg, page = 1 << p.shift;
+  const int64_t limit = p.c.n_pages << p.shift;
+  if (warp == 0) {
+    const int t = t0 + lane;
+    bool start = false;
+    if (lane < p.seg && t < p.T) {
+      const int s = __ldg(p.slots + t);
+      if (s >= limit) record_status(p.status, WINA_ERR_INVALID_ARG);
+      start = s >= 0 && s < limit && ((s & (page - 1)) == 0 || t == 0 || __ldg(p.slots + t - 1) != s - 1);
+    }
+    const unsigned m = __ballot_sync(0xffffffffu, start);
+    if (start) s_run[__popc(m & ((1u << lane) - 1u))] = t;
+    if (lane == 0) s_n = __popc(m);
+  }
+  __syncthreads();
+  // the runs' lengths: consecutive tokens at consecutive places of the page
+  for (int r = warp; r < s_n; r += kWriteW) {
+    const int t = s_run[r], slot = __ldg(p.slots + t), first = slot & (page - 1);
+    int len = 1;
+    for (int base = 1; base < page - first; base += 32) {
+      const int i = base + lane;
+      const bool on = i < page - first && t + i < p.T && __ldg(p.slots + t + i) == slot + i;
+      const unsigned m = __ballot_sync(0xffffffffu, on);
+      const int more = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
+      len += more;
+      if (more < 32) break;
+    }
+    if (lane == 0) s_len[r] = len;
+  }
+  __syncthreads();
+  const int heads = (int)p.c.heads, H2 = 2 * heads;
+  const int sub = lane / LPR, ch = (lane % LPR) * 8;
+
+  // an item by `nw` warps (1 or all), of which this is warp w
+  auto item = [&](int r, int hh, int w, int nw) {
+    const int t = s_run[r], len = s_len[r], which = hh / heads, h = hh % heads;
+    const int slot = __ldg(p.slots + t), first = slot & (page - 1), pg = slot >> p.shift;
+    const void* x = which ? p.x[1] : p.x[0];
+    const int64_t ld = which ? p.ld[1] : p.ld[0], src = (int64_t)t * ld + (int64_t)h * DH + ch;
+    float* scale_at = (which ? p.c.v_scale : p.c.k_scale) + (int64_t)pg * p.c.heads + h;
+    uint8_t* dst = reinterpret_cast<uint8_t*>(which ? p.c.v : p.c.k) + (((int64_t)pg * p.c.heads + h) << p.shift) * DH + ch;
+    const float present = first ? *scale_at : 0.f;
+    Row8<BF16> row[IT];
+    auto load = [&](int i0) {
+#pragma unroll
+      for (int q = 0; q < IT; ++q) {
+        const int i = i0 + q * RPP + sub;
+        if (i < len) row[q].load(x, src + (int64_t)i * ld);
+      }
+    };
+    uint32_t amax = 0;  // magnitudes order like their bits, NaN above all (bf16: two maxima side by side)
+    for (int i0 = w * ROWS; i0 < len; i0 += nw * ROWS) {
+      load(i0);
+#pragma unroll
+      for (int q = 0; q < IT; ++q)
+        if (i0 + q * RPP + sub < len) row[q].amax(amax);
+    }
+    if constexpr (BF16) amax = max(amax & 0xffffu, amax >> 16) << 16;
+    amax = __reduce_max_sync(0xffffffffu, amax);
+    if (nw > 1) {
+      if (lane == 0) s_amax[w] = amax;
+      __syncthreads();  // everybody has read the present scale, too
+#pragma unroll
+      for (int k = 0; k < kWriteW; ++k) amax = max(amax, s_amax[k]);
+    }
+    const bool lost = amax >= 0x7f800000u || present != present;  // no scale holds these rows
+    float s;
+    if (lost) {
+      s = __uint_as_float(0x7fc00000u);
+    } else {
+      s = pow2_scale<E4M3>(amax);
+      if (first && present > s) s = present;
+    }
+    if (first && !lost && s != present) {
+      // the scale grew: the page's older rows, rounded again
+      const float f = __fdiv_rn(present, s);
+      for (int i = w * RPP + sub; i < first; i += nw * RPP) {
+        uint2 v = *reinterpret_cast<const uint2*>(dst + i * DH);
+        float a[4], b[4];
+        unpack4<E4M3>(v.x, a);
+        unpack4<E4M3>(v.y, b);
+        v.x = pack4<E4M3>(a[0] * f, a[1] * f, a[2] * f, a[3] * f);
+        v.y = pack4<E4M3>(b[0] * f, b[1] * f, b[2] * f, b[3] * f);
+        *reinterpret_cast<uint2*>(dst + i * DH) = v;
+      }
+    }
+    const float inv = lost ? 0.f : __fdiv_rn(1.f, s);
+    const bool again = len > nw * ROWS;
+    for (int i0 = w * ROWS; i0 < len; i0 += nw * ROWS) {
+      if (again) load(i0);
+#pragma unroll
+      for (int q = 0; q < IT; ++q) {
+        const int i = i0 + q * RPP + sub;
+        if (i < len) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = row[q].get(e) * inv;
+          const uint2 bytes = make_uint2(pack4<E4M3>(v[0], v[1], v[2], v[3]), pack4<E4M3>(v[4], v[5], v[6], v[7]));
+          *reinterpret_cast<uint2*>(dst + (first + i) * DH) = lost ? make_uint2(0, 0) : bytes;
+        }
+      }
+    }
+    if (w == 0 && lane == 0 && (first == 0 || s != present)) *scale_at = s;
+    if (nw > 1) __syncthreads();  // s_amax is free again
+  };
+
+  for (int it = blockIdx.y * kWriteW + warp; it < s_n * H2; it += gridDim.y * kWriteW)
+    if (s_len[it / H2] <= ROWS) item(it / H2, it % H2, 0, 1);
+  for (int it = blockIdx.y; it < s_n * H2; it += gridDim.y)
+    if (s_len[it / H2] > ROWS) item(it / H2, it % H2, warp, kWriteW);
 }
 
 // ------------------------------------------------------------------------------------
@@ -364,59 +497,72 @@ struct ReadParams {
   kv8_cache_t c;
   const int32_t* slots;
   void* out[2];
-  int64_t pieces;  // 16-channel pieces of one of the two
-  int shift, log_row;  // pieces of a head's row: 1 << log_row
+  int T, shift;
+  int per_token, log_head;  // pieces of a token's row, and (as a shift) of a head's
   int32_t* status;
 };
 
-// 16 channels per thread: one 16-byte load, two (bf16) or four (float32) 16-byte stores.
-// HBM-bound; a page's place is found once per piece, from L1.
+constexpr int kReadT = 256;  // threads per CTA
+constexpr int kReadU = 4;    // pieces of a thread, their loads in flight together
+
+// A piece is 16 bytes of the output: 8 channels (bf16) or 4 (float32), so that a warp's stores
+// are whole lines; its 8 (4) bytes are loaded likewise. A CTA takes kReadT * kReadU consecutive
+// pieces of the rows of one side. HBM-bound.
 template <bool BF16, bool E4M3>
-__global__ void __launch_bounds__(256) k_kv8_read(ReadParams p) {
+__global__ void __launch_bounds__(kReadT) k_kv8_read(ReadParams p) {
+  constexpr int VEC = BF16 ? 8 : 4;
   const int64_t limit = p.c.n_pages << p.shift;
-  const int which = blockIdx.y;
+  const bool which = blockIdx.y != 0;
   const uint8_t* src = reinterpret_cast<const uint8_t*>(which ? p.c.v : p.c.k);
   const float* scales = which ? p.c.v_scale : p.c.k_scale;
   void* const out = which ? p.out[1] : p.out[0];
   if (!out) return;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.pieces; i += (int64_t)gridDim.x * 256) {
-    const int64_t row = i >> p.log_row;  // token * heads + head
-    const int64_t t = row / p.c.heads;
-    const int h = (int)(row - t * p.c.heads);
-    const int s = __ldg(p.slots + t);
-    float f[16];
-    if (s >= 0 && s < limit) {
-      const int pg = s >> p.shift, off = s & ((1 << p.shift) - 1);
-      const int64_t head = (int64_t)pg * p.c.heads + h;
-      const uint4 w = *reinterpret_cast<const uint4*>(src + ((((head << p.shift) + off) << p.log_row) + (i & ((1 << p.log_row) - 1))) * 16);
-      const float sc = scales[head];
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  // the first piece's token, once per CTA; the rest by 32-bit arithmetic
+  const int64_t first = (int64_t)blockIdx.x * (kReadT * kReadU);
+  const int64_t t0 = first / p.per_token;
+  const unsigned in0 = (unsigned)(first - t0 * p.per_token) + threadIdx.x;
+  uint2 w[kReadU];
+  float sc[kReadU];
+  bool live[kReadU];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float a[4];
-        unpack4<E4M3>(u[q], a);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f[4 * q + e] = a[e] * sc;
+  for (int u = 0; u < kReadU; ++u) {
+    const unsigned i = in0 + u * kReadT, dt = i / (unsigned)p.per_token, j = i - dt * (unsigned)p.per_token;
+    const int64_t t = t0 + dt;
+    w[u] = make_uint2(0, 0);
+    sc[u] = 0.f;
+    live[u] = t < p.T;
+    if (live[u]) {
+      const int s = __ldg(p.slots + t);
+      if (s >= 0 && s < limit) {
+        const int64_t head = (int64_t)(s >> p.shift) * p.c.heads + (j >> p.log_head);
+        const uint8_t* at = src + ((head << p.shift) + (s & ((1 << p.shift) - 1))) * p.c.dh + (j & ((1u << p.log_head) - 1)) * VEC;
+        if constexpr (BF16) w[u] = __ldg(reinterpret_cast<const uint2*>(at));
+        else w[u].x = __ldg(reinterpret_cast<const uint32_t*>(at));
+        sc[u] = __ldg(scales + head);
+      } else if (s >= limit) {
+        record_status(p.status, WINA_ERR_INVALID_ARG);
       }
-    } else {
-      if (s >= limit) record_status(p.status, WINA_ERR_INVALID_ARG);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) f[e] = 0.f;
     }
+  }
+#pragma unroll
+  for (int u = 0; u < kReadU; ++u) {
+    if (!live[u]) continue;
+    uint4* d = reinterpret_cast<uint4*>(out) + first + threadIdx.x + u * kReadT;
+    float a[4];
+    unpack4<E4M3>(w[u].x, a);
     if constexpr (BF16) {
-      uint4* d = reinterpret_cast<uint4*>(out) + i * 2;
-      uint32_t o[8];
+      float b[4];
+      unpack4<E4M3>(w[u].y, b);
+      uint32_t o[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
-        o[e] = *reinterpret_cast<const uint32_t*>(&b);
+      for (int e = 0; e < 4; ++e) {
+        const float* f = e < 2 ? a : b;
+        const __nv_bfloat162 x = __floats2bfloat162_rn(f[(2 * e) & 3] * sc[u], f[(2 * e + 1) & 3] * sc[u]);
+        o[e] = *reinterpret_cast<const uint32_t*>(&x);
       }
-      d[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      *d = make_uint4(o[0], o[1], o[2], o[3]);
     } else {
-      float4* d = reinterpret_cast<float4*>(out) + i * 4;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) d[q] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+      *d = make_uint4(__float_as_uint(a[0] * sc[u]), __float_as_uint(a[1] * sc[u]), __float_as_uint(a[2] * sc[u]), __float_as_uint(a[3] * sc[u]));
     }
   }
 }
@@ -474,9 +620,16 @@ extern "C" wina_status_t kv8_plan(const int32_t* seq_len, const int32_t* new_len
   return cuda_status(cudaLaunchKernelEx(&cfg, k_kv8_plan, p));
 }
 
+template <bool BF16, bool E4M3, int DH>
+static void (*write_kernel(int64_t page))(WriteParams) {
+  constexpr int ROWS = (BF16 ? 8 : 4) * (32 / (DH / 8));  // rows that a warp holds
+  return page > 4 * ROWS ? k_kv8_write_shared<BF16, E4M3, DH> : k_kv8_write<BF16, E4M3, DH>;
+}
+
 template <bool BF16, bool E4M3>
-static void (*write_kernel(int64_t dh))(WriteParams) {
-  return dh == 64 ? k_kv8_write<BF16, E4M3, 64> : dh == 128 ? k_kv8_write<BF16, E4M3, 128> : k_kv8_write<BF16, E4M3, 256>;
+static void (*write_kernel(int64_t dh, int64_t page))(WriteParams) {
+  return dh == 64 ? write_kernel<BF16, E4M3, 64>(page)
+                  : dh == 128 ? write_kernel<BF16, E4M3, 128>(page) : write_kernel<BF16, E4M3, 256>(page);
 }
 
 extern "C" wina_status_t kv8_write(const kv8_cache_t* cache, const void* k, const void* v, wina_dtype_t xdt, int64_t T,
@@ -507,11 +660,13 @@ extern "C" wina_status_t kv8_write(const kv8_cache_t* cache, const void* k, cons
   const int64_t sms = device_sm_count();
   if (sms < 1) return WINA_ERR_CUDA;
   p.seg = (int)std::max<int64_t>(1, std::min<int64_t>(kWriteSeg, T / sms));
+  // the items of a stretch of tokens over several CTAs: eight at least, and more where few CTAs
+  // would be running
   const int64_t gx = (T + p.seg - 1) / p.seg, most = 2 * cache->heads;
-  const int64_t gy = (most + kWriteW - 1) / kWriteW;
+  const int64_t gy = std::min(most, std::max((most + kWriteW - 1) / kWriteW, (8 * sms + gx - 1) / gx));
   const bool e4 = cache->format == KV8_E4M3;
-  void (*kern)(WriteParams) = xdt == WINA_BF16 ? (e4 ? write_kernel<true, true>(cache->dh) : write_kernel<true, false>(cache->dh))
-                                               : (e4 ? write_kernel<false, true>(cache->dh) : write_kernel<false, false>(cache->dh));
+  void (*kern)(WriteParams) = xdt == WINA_BF16 ? (e4 ? write_kernel<true, true>(cache->dh, cache->page) : write_kernel<true, false>(cache->dh, cache->page))
+                                               : (e4 ? write_kernel<false, true>(cache->dh, cache->page) : write_kernel<false, false>(cache->dh, cache->page));
   kern<<<dim3((unsigned)gx, (unsigned)gy), 32 * kWriteW, 0, (cudaStream_t)stream>>>(p);
   return cuda_status(cudaGetLastError());
 }
@@ -530,16 +685,18 @@ extern "C" wina_status_t kv8_read(const kv8_cache_t* cache, const int32_t* slots
   p.slots = slots;
   p.out[0] = k;
   p.out[1] = v;
-  p.log_row = cache->dh == 64 ? 2 : cache->dh == 128 ? 3 : 4;
-  p.pieces = T * cache->heads << p.log_row;
+  p.T = (int)T;
+  const int vec = xdt == WINA_BF16 ? 8 : 4;
+  p.per_token = (int)(cache->heads * cache->dh / vec);
+  p.log_head = (cache->dh == 64 ? 6 : cache->dh == 128 ? 7 : 8) - (vec == 8 ? 3 : 2);
   p.shift = page_shift(cache->page);
   p.status = status_dev;
-  const int sms = device_sm_count();
-  if (sms < 1) return WINA_ERR_CUDA;
-  const dim3 grid((unsigned)std::min<int64_t>((p.pieces + 255) / 256, (int64_t)sms * 16), 2);
+  const int64_t blocks = (T * p.per_token + kReadT * kReadU - 1) / (kReadT * kReadU);
+  if (blocks > INT32_MAX) return WINA_ERR_INVALID_ARG;
+  const dim3 grid((unsigned)blocks, 2);
   const bool e4 = cache->format == KV8_E4M3;
   void (*kern)(ReadParams) = xdt == WINA_BF16 ? (e4 ? k_kv8_read<true, true> : k_kv8_read<true, false>)
                                               : (e4 ? k_kv8_read<false, true> : k_kv8_read<false, false>);
-  kern<<<grid, 256, 0, (cudaStream_t)stream>>>(p);
+  kern<<<grid, kReadT, 0, (cudaStream_t)stream>>>(p);
   return cuda_status(cudaGetLastError());
 }

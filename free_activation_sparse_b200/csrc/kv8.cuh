@@ -71,6 +71,12 @@ struct Row8 {
       w[1] = __ldg(s + 1);
     }
   }
+  // a becomes the largest magnitude's bits: of bf16 rows, of the even and of the odd elements
+  __device__ __forceinline__ void amax(uint32_t& a) const {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 4 : 8); ++i) a = BF16 ? __vmaxu2(a, u[i] & 0x7fff7fffu) : max(a, u[i] & 0x7fffffffu);
+  }
   __device__ __forceinline__ float get(int i) const {
     const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
     if constexpr (BF16) return __uint_as_float((i & 1) ? (u[i >> 1] & 0xffff0000u) : (u[i >> 1] << 16));
