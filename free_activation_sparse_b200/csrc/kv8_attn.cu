@@ -186,6 +186,10 @@ __global__ void __launch_bounds__(SplitShape<BF16, DH, NT>::THREADS, 1)
   enter(w);
   if (lane == 0) s_walk[warp] = w;
   __syncwarp();
+  // offsets of this lane's pieces: of its first copy, its key rows and its value rows
+  constexpr int RB = DH == 64 ? 64 : 128;  // bytes from row to row of a staged block
+  const uint32_t in_group = staged<DH>(lane / (DH / 16), lane % (DH / 16));
+  const uint32_t k_at = staged<DH>(g, DH == 64 ? t : 2 * t), v_at = staged<DH>(2 * t, DH == 64 ? g >> 1 : g);
   // one chunk into `slot`
   auto issue = [&](int slot) {
     while (more && pc >= pto) {  // the next tile with a chunk for this warp
@@ -214,16 +218,35 @@ __global__ void __launch_bounds__(SplitShape<BF16, DH, NT>::THREADS, 1)
       }
       if (bad && lane == 0) record_status(p.status, WINA_ERR_INVALID_ARG);
       const uint32_t dst = tc::smem_u32(sm + (size_t)(warp * S + slot) * STAGE);
-      constexpr int PPR = DH / 16;  // 16-byte pieces per row
+      constexpr int PPR = DH / 16, RPI = 32 / PPR, N = 16 / RPI;  // pieces of a row, rows and passes of a warp
+      bool inside = key0 >= plo && key0 + CH <= phi;
 #pragma unroll
-      for (int i = 0; i < CH * PPR / 32; ++i) {
-        const int piece = i * 32 + lane, row = piece / PPR, key = key0 + row;
-        const int64_t h = head[MT == 2 ? (i * 32 / PPR) / 16 : 0];  // the 32 pieces lie in one group
-        const bool on = h >= 0 && key >= plo && key < phi;
-        const int64_t from = on ? ((h << p.shift) + (key & page_mask)) * DH + (piece % PPR) * 16 : 0;
-        const uint32_t d = dst + (row / 16) * 16 * DH + staged<DH>(row % 16, piece % PPR);
-        cp_async16(d, reinterpret_cast<const uint8_t*>(p.c.k) + from, on ? 16 : 0, pol);
-        cp_async16(d + CH * DH, reinterpret_cast<const uint8_t*>(p.c.v) + from, on ? 16 : 0, pol);
+      for (int u = 0; u < MT; ++u) inside = inside && head[u] >= 0;
+      if (inside) {
+        // a group is one run of a page: fixed offsets from one address
+#pragma unroll
+        for (int u = 0; u < MT; ++u) {
+          const int64_t from = ((head[u] << p.shift) + ((key0 + 16 * u) & page_mask)) * DH + lane * 16;
+          const uint8_t *sk = reinterpret_cast<const uint8_t*>(p.c.k) + from, *sv = reinterpret_cast<const uint8_t*>(p.c.v) + from;
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const uint32_t d = dst + u * 16 * DH + (in_group ^ (DH == 64 ? 0 : ((i * RPI) & 7) << 4)) + i * RPI * RB;
+            cp_async16(d, sk + 512 * i, 16, pol);
+            cp_async16(d + CH * DH, sv + 512 * i, 16, pol);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < MT; ++u)
+#pragma unroll 1
+          for (int i = 0; i < N; ++i) {
+            const int row = i * RPI + lane / PPR, key = key0 + 16 * u + row;
+            const bool on = head[u] >= 0 && key >= plo && key < phi;
+            const int64_t from = on ? ((head[u] << p.shift) + (key & page_mask)) * DH + (lane % PPR) * 16 : 0;
+            const uint32_t d = dst + u * 16 * DH + staged<DH>(row, lane % PPR);
+            cp_async16(d, reinterpret_cast<const uint8_t*>(p.c.k) + from, on ? 16 : 0, pol);
+            cp_async16(d + CH * DH, reinterpret_cast<const uint8_t*>(p.c.v) + from, on ? 16 : 0, pol);
+          }
       }
       if (lane < 2 * MT) {
         const int64_t h = (MT == 2 && (lane & 1)) ? head[MT - 1] : head[0];
@@ -330,9 +353,10 @@ __global__ void __launch_bounds__(SplitShape<BF16, DH, NT>::THREADS, 1)
       for (int u = 0; u < MT; ++u)
 #pragma unroll
         for (int j = 0; j < KC; ++j) {
-          const int cc = DH == 64 ? t : (j >> 1) * 8 + 2 * t + (j & 1);
-          const uint4 x = *reinterpret_cast<const uint4*>(kst + u * 16 * DH + staged<DH>(g, cc));
-          const uint4 y = *reinterpret_cast<const uint4*>(kst + u * 16 * DH + staged<DH>(g + 8, cc));
+          // piece 2 t + (j & 1) of block j / 2 (DH 64: piece t); row g + 8 is permuted like row g
+          const unsigned char* at = kst + u * 16 * DH + (j >> 1) * 2048 + (k_at ^ ((j & 1) << 4));
+          const uint4 x = *reinterpret_cast<const uint4*>(at);
+          const uint4 y = *reinterpret_cast<const uint4*>(at + 8 * RB);
           const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -452,13 +476,14 @@ __global__ void __launch_bounds__(SplitShape<BF16, DH, NT>::THREADS, 1)
           uint32_t x[4][VW];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int row = 2 * t + (k & 1) + (k >> 1) * 8;
+            // row 2 t + (k & 1) + 8 (k >> 1)
+            const unsigned char* at = vst + u * 16 * DH + h * 2048 + (v_at ^ (DH == 64 ? 0 : (k & 1) << 4)) + ((k & 1) + (k >> 1) * 8) * RB;
             if constexpr (DH == 64) {
-              const uint2 v = *reinterpret_cast<const uint2*>(vst + u * 16 * DH + staged<DH>(row, g >> 1) + (g & 1) * 8);
+              const uint2 v = *reinterpret_cast<const uint2*>(at + (g & 1) * 8);
               x[k][0] = v.x;
               x[k][1] = v.y;
             } else {
-              const uint4 v = *reinterpret_cast<const uint4*>(vst + u * 16 * DH + staged<DH>(row, h * 8 + g));
+              const uint4 v = *reinterpret_cast<const uint4*>(at);
               x[k][0] = v.x;
               x[k][1] = v.y;
               x[k][2] = v.z;
