@@ -69,11 +69,16 @@ __device__ __forceinline__ bool bad_req(const AttnParams& p, int b) {
   return bad || kv < 0 || kv > room;
 }
 
+constexpr unsigned kEmptyCost = 4;
+
 // The keys [lo, hi) that rows r0 .. r0 + R - 1 of a request see (row = query * G + head in
-// the group), and the chunks of CH keys they lie in. A tile that sees nothing has one chunk
-// with no keys, so that its rows get their zeros on the common path.
+// the group), and the chunks of CH keys they lie in; none for a tile that sees nothing.
 struct Span {
   int lo, hi, c0, c1;
+  // Units on the line of work: the chunks, and what a tile costs besides (its queries, the
+  // joining of its parts), p.tile_cost, before its first chunk; kEmptyCost where rows only get
+  // zeros (in a request with keys; one without any is not on the line).
+  __device__ __forceinline__ unsigned len(const AttnParams& p) const { return c1 > c0 ? (unsigned)(c1 - c0 + p.tile_cost) : kEmptyCost; }
 };
 
 template <int R, int CH>
@@ -83,8 +88,7 @@ __device__ __forceinline__ Span tile_span(const AttnParams& p, const Req& r, int
   s.hi = r.kv - r.n + r1 / p.G + 1;
   s.lo = p.window > 0 ? max(0, r.kv - r.n + r0 / p.G - p.window + 1) : 0;
   if (s.hi <= s.lo) {
-    s.lo = s.hi = s.c0 = 0;
-    s.c1 = 1;
+    s.lo = s.hi = s.c0 = s.c1 = 0;
   } else {
     s.c0 = s.lo / CH;
     s.c1 = (s.hi + CH - 1) / CH;
@@ -94,19 +98,28 @@ __device__ __forceinline__ Span tile_span(const AttnParams& p, const Req& r, int
 
 template <int R>
 __device__ __forceinline__ int tiles_of(const AttnParams& p, const Req& r) {
-  return (r.nq * p.G + R - 1) / R;
+  return r.kv ? (r.nq * p.G + R - 1) / R : 0;
 }
 
-// Cost of all of a request's tiles, for one kv head. p.tile_cost is what a tile costs besides
-// its chunks (its queries, the joining of its parts), in chunks; it lies before the tile's
-// first chunk on the line of work.
+// Zeros for the requests without keys (a padded batch's places), dealt over the grid.
+template <bool BF16>
+__device__ __forceinline__ void zero_rows(const AttnParams& p) {
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    const Req r = load_req(p, b);
+    if (r.kv) continue;
+    const int64_t row = (int64_t)p.Hq * p.c.dh * (BF16 ? 2 : 4) / 16;  // 16-byte pieces of a query
+    uint4* d = reinterpret_cast<uint4*>(p.out) + r.q0 * row;
+    for (int64_t i = threadIdx.x; i < r.nq * row; i += blockDim.x) d[i] = make_uint4(0, 0, 0, 0);
+  }
+}
+
+// Units of all of a request's tiles, for one kv head.
 template <int R, int CH>
 __device__ __forceinline__ unsigned long long req_cost(const AttnParams& p, const Req& r) {
   const int nt = tiles_of<R>(p, r);
   unsigned long long c = 0;
   for (int t = 0; t < nt; ++t) {
-    const Span s = tile_span<R, CH>(p, r, t);
-    c += s.c1 - s.c0 + p.tile_cost;
+    c += tile_span<R, CH>(p, r, t).len(p);
   }
   return c;
 }
@@ -150,7 +163,11 @@ struct Walk {
   Span s;
   unsigned long long at;  // the line's units before this tile
 
-  __device__ __forceinline__ unsigned len(const AttnParams& p) const { return (unsigned)(s.c1 - s.c0 + p.tile_cost); }
+  __device__ __forceinline__ unsigned len(const AttnParams& p) const { return s.len(p); }
+  // whether the tile's rows only get zeros, and the team of units [u0, u1) is to write them
+  __device__ __forceinline__ bool empty_of(unsigned long long u0, unsigned long long u1) const {
+    return s.c0 == s.c1 && at >= u0 && at < u1;
+  }
 
   // the tile that holds unit u
   __device__ __forceinline__ void locate(const AttnParams& p, const uint32_t* pre, unsigned long long u) {
@@ -187,8 +204,7 @@ struct Walk {
       if (++hk == (int)p.c.heads) {
         hk = 0;
         do r = load_req(p, ++b);
-        while (r.nq == 0 && b < p.B - 1);
-        nt = tiles_of<R>(p, r);
+        while ((nt = tiles_of<R>(p, r)) == 0 && b < p.B - 1);
       }
     }
     s = tile_span<R, CH>(p, r, tile);

@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
   }
   const bool fits = cost_prefix<kThreads, kRows, kKeys>(p, pre, red);
   const unsigned long long C = (unsigned long long)pre[pre_entries(p.B) - 1] * p.c.heads;
+  if (fits) zero_rows<true>(p);
   if (!fits || C == 0) {
     if (!fits && blockIdx.x == 0 && tid == 0) record_status(p.status, WINA_ERR_INVALID_ARG);
     return;
@@ -471,10 +472,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
         const int last_low = max(w.s.lo, p.window > 0 ? pos0 + last_row / p.G + 1 - p.window : 0);
         float m = -INFINITY, l = 0.f, sref = 0.f;
         for (int c = from; c < to; ++c, ++it) {
-          wait(&info_full[it % kInfo], (uint32_t)((it / kInfo) & 1));
-          const Info info = s_info[it % kInfo];
           wait(&s_full[h], (uint32_t)(sn++ & 1));
           tc::tc_fence_after();
+          // after S, so that the barrier is at this chunk's phase: a half that had no rows in the
+          // tile before comes here many phases early, and could not tell them apart
+          wait(&info_full[it % kInfo], (uint32_t)((it / kInfo) & 1));
+          const Info info = s_info[it % kInfo];
           const int key0 = c * kKeys;
           const bool masked = info.bad || key0 < last_low || key0 + kKeys > first_lim;
           const float cf = fac * info.kfac;
@@ -598,6 +601,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
         tc::tc_fence_before();  // O has been read before the next tile's first product, which waits for P
       } else {
         it += max(0, to - from);  // the other half's chunks
+        if (w.empty_of(u0, u1))
+          for (int j = tid; j < rows * DH / 4; j += 256)
+            store_row<true>(p, w.r, w.hk, w.tile * kRows + j / (DH / 4), (j % (DH / 4)) * 4, make_float4(0.f, 0.f, 0.f, 0.f), 0.f);
       }
       if (from < to && !(from == w.s.c0 && to == w.s.c1)) {
         // both halves together: the last of the tile's teams joins the parts in order

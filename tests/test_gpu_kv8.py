@@ -492,6 +492,24 @@ def test_attention_large_batches_and_long_contexts(B, kv_max, hq, hkv, q_max, dt
                         [0, ql[b]], dtype)
 
 
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("B,kv_max,hq,hkv,q_max,dh", [(40, 3000, 8, 2, 80, 128), (25, 4000, 8, 8, 140, 128), (4, 6000, 32, 8, 1500, 128),
+                                                      (30, 2500, 16, 2, 33, 64), (300, 500, 4, 4, 70, 64)])
+def test_attention_bf16_prompts_agree_with_float32_everywhere(B, kv_max, hq, hkv, q_max, dh, fmt):
+    """Long lines of tiles of every height, many to a CTA: every row of the bf16 path against the
+    float32 path (another kernel) on the same numbers, within bf16's half step of a result and
+    2^-11 of each weight; the rows' sizes stand in for their mass."""
+    rng = np.random.default_rng(B + q_max)
+    kv = rng.integers(kv_max // 3, kv_max + 1, size=B).tolist()
+    ql = [int(min(n, rng.integers(1, q_max + 1))) for n in kv]
+    m, q, table, cu = attention_case(B + 1, kv, ql, hq, hkv, dh, 16, fmt, "bf16")
+    args = (dev_i32(table), dev_i32(np.array(kv)))
+    a = W.kv8_attention(m.c, q, *args, cu_q=dev_i32(cu), max_q=max(ql)).float()
+    b = W.kv8_attention(m.c, q.float(), *args, cu_q=dev_i32(cu), max_q=max(ql))
+    rel = ((a - b).norm(dim=2) / b.norm(dim=2)).max()
+    assert float(rel) <= 2.0 ** -7, float(rel)  # 2^-8, and as much again for the weights' errors against the norm
+
+
 def test_attention_offsets_past_32_bits():
     """A cache of more than 2^32 bytes a side whose last pages are the ones in use."""
     t = torch()
