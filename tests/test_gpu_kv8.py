@@ -510,6 +510,22 @@ def test_attention_bf16_prompts_agree_with_float32_everywhere(B, kv_max, hq, hkv
     assert float(rel) <= 2.0 ** -7, float(rel)  # 2^-8, and as much again for the weights' errors against the norm
 
 
+@pytest.mark.parametrize("dtype,dh,hq,hkv,q_max", [("bf16", 128, 4, 1, 1), ("f32", 128, 16, 1, 1), ("f32", 64, 2, 2, 1),
+                                                    ("bf16", 256, 2, 1, 5), ("bf16", 128, 40, 1, 3)])
+def test_attention_most_requests(dtype, dh, hq, hkv, q_max):
+    """8192 requests: the largest shared memory of every shape; sampled requests."""
+    rng = np.random.default_rng(dh)
+    kv = rng.integers(0, 40, size=8192).tolist()
+    ql = [int(min(max(n, 1), rng.integers(1, q_max + 1))) for n in kv]
+    m, q, table, cu = attention_case(3, kv, ql, hq, hkv, dh, 16, "int8", dtype)
+    st = status_word()
+    out = W.kv8_attention(m.c, q, dev_i32(table), dev_i32(np.array(kv)), cu_q=dev_i32(cu), max_q=q_max, status=st)
+    assert int(host(st)[0]) == 0
+    for b in sorted({0, 1, 2, 8190, 8191, *rng.integers(0, 8192, size=40).tolist()}):
+        a, e = int(cu[b]), int(cu[b + 1])
+        check_attention(out[a:e], m, q[a:e], table[b:b + 1], kv[b:b + 1], [0, e - a], dtype)
+
+
 def test_attention_offsets_past_32_bits():
     """A cache of more than 2^32 bytes a side whose last pages are the ones in use."""
     t = torch()
