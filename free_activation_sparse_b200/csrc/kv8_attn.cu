@@ -3,9 +3,10 @@
 //   s_j = (q . k8_j) ks[page_j] scale;  out = sum_j p_j vs[page_j] v8_j / sum_j p_j,
 //   p_j = exp(s_j - max)
 //
-// k_kv8_attn_split: single tokens, short spans, and float32 prompts. Bound by HBM: every key
-// and value byte is read once per block of 8 or 16 query rows (the rows of a kv head's query
-// group, so grouped queries share the read).
+// Two kernels. k_kv8_attn_split (here): single tokens, short spans, rows 256 wide, and float32
+// prompts; bound by HBM: every key and value byte is read once per block of 8 or 16 query rows
+// (the rows of a kv head's query group, so grouped queries share the read).
+// k_kv8_attn_prompt (kv8_prompt.cu): prompt chunks of bf16 queries, on the tensor cores.
 #include <math.h>
 
 #include <algorithm>
@@ -686,7 +687,7 @@ static size_t split_slot_floats(int64_t dh, int64_t rows) { return (size_t)split
 
 size_t kv8_attention_ws_size(int64_t dh, int64_t rows) {
   size_t slots = (size_t)2 * kMaxTeams * split_slot_floats(dh, rows);
-  if (prompt_takes(true, dh, rows)) slots = std::max(slots, (size_t)2 * kMaxCtas * prompt_slot_floats(dh));
+  if (prompt_takes(true, dh, rows, INT64_MAX)) slots = std::max(slots, (size_t)2 * kMaxCtas * prompt_slot_floats(dh));
   return round_up((size_t)kMaxTeams * 4, kAlign) + round_up(slots * 4, kAlign);
 }
 
@@ -781,6 +782,6 @@ extern "C" wina_status_t kv8_attention(const kv8_cache_t* cache, const void* q, 
   p.counters = reinterpret_cast<uint32_t*>(ws);
   p.slots = reinterpret_cast<float*>((char*)ws + round_up((size_t)kMaxTeams * 4, kAlign));
   const int64_t rows = max_q * (Hq / cache->heads);
-  if (prompt_takes(qdt == WINA_BF16, cache->dh, rows)) return launch_prompt(p, rows, (cudaStream_t)stream);
+  if (prompt_takes(qdt == WINA_BF16, cache->dh, rows, T * Hq)) return launch_prompt(p, (cudaStream_t)stream);
   return launch_split(p, qdt == WINA_BF16, rows, (cudaStream_t)stream);
 }

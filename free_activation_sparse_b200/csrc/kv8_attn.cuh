@@ -265,10 +265,11 @@ __device__ __forceinline__ void store_row(const AttnParams& p, const Req& r, int
 }
 
 // The kernel for long rows of bf16 queries (kv8_prompt.cu): whether it takes a call with up to
-// `rows` query rows a request and kv head, the floats of one of its slots, and its launch.
-bool prompt_takes(bool bf16, int64_t dh, int64_t rows);
+// `rows` query rows a request and kv head and `all_rows` over all, the floats of one of its
+// slots, and its launch.
+bool prompt_takes(bool bf16, int64_t dh, int64_t rows, int64_t all_rows);
 size_t prompt_slot_floats(int64_t dh);
-wina_status_t launch_prompt(AttnParams& p, int64_t rows, cudaStream_t s);
+wina_status_t launch_prompt(AttnParams& p, cudaStream_t s);
 
 constexpr int kMaxCtas = 160;  // CTAs of either kernel, one per SM, at most
 

@@ -19,6 +19,7 @@ constexpr int kRows = 256;        // query rows of a tile: two halves of 128
 constexpr int kKeys = 128;        // keys of a chunk
 constexpr int kThreads = 640;     // warps 0-3, 4-7: softmax of a half; 8-15: bytes; 16: matrix products
 constexpr int kInfo = 4;          // chunks whose factors are kept
+constexpr int kPartMin = 4;       // units of the line of work in a CTA's part, at least
 // Registers a thread, of the 96 (640 threads) that it is launched with.
 constexpr int kLaunchRegs = 96, kSoftmaxRegs = 136, kByteRegs = 80, kMmaRegs = 40;
 static_assert(256 * kSoftmaxRegs + 256 * kByteRegs + 128 * kMmaRegs <= kThreads * kLaunchRegs, "register split");
@@ -29,7 +30,6 @@ constexpr float kGrow = 16.f;     // until a scale is 16 times as large
 
 template <int DH>
 struct PromptShape {
-  static constexpr int HALVES = DH / 64;                   // 128-byte blocks of a row of 16-bit numbers
   static constexpr int TILE = kKeys * DH * 2;              // bytes of a chunk's keys (values) as float16
   static constexpr int QTILE = 128 * DH * 2;               // bytes of a half's queries
   static constexpr size_t SMEM = 1024 + 2 * QTILE + 4 * TILE;
@@ -149,7 +149,16 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 //     weights as float16 in a second; O is rescaled only when a maximum outgrows its
 //     reference by 2^8 (a weight keeps 11 bits from 2^15 down to 2^-14).
 // Queries are float16 times a power of two per row (exact for bf16 within 2^28 of the row's
-// largest). Places without a page or outside the tile's keys are zeros.
+// largest). Places without a page or outside the tile's keys are zeros. A half whose bytes of a
+// page are no numbers (kv8_write stores none) may get NaN where it does not see them.
+//
+// 4 chunks of up to 2048 queries behind 2 K to 6 K keys (32 / 8 heads of 128, 0.52 TFLOP): 0.79 ms,
+// 658 TFLOP/s; a step of 128 keys takes 5.4 K cycles, of which the tensor cores work 2.1 K. What
+// holds it is the chain of a half: products 1.6 K cycles with their hand-overs, maxima 0.9 K,
+// weights 2.5 K; with the conversions, the exponentials and the first pass left out together it
+// still takes 0.70 ms. Slower: four softmax warps a quarter (1.02 ms, spills), S by 64 keys in
+// two places a half (1.00 ms, twice the hand-overs), both passes unrolled (1.23 ms, instruction
+// caches), four warps for the bytes (1.74 ms).
 template <bool E4M3, int DH>
 __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParams p) {
   using Sh = PromptShape<DH>;
@@ -189,7 +198,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
     if (!fits && blockIdx.x == 0 && tid == 0) record_status(p.status, WINA_ERR_INVALID_ARG);
     return;
   }
-  const int nc = (int)min((unsigned long long)gridDim.x, C), team = blockIdx.x;  // every team has a unit
+  // a team's part is worth kPartMin units, so that few tiles are not cut into many parts to join
+  const int nc = (int)min((unsigned long long)gridDim.x, max(1ull, C / kPartMin)), team = blockIdx.x;
   if (team >= nc) return;
   if (warp == 16) tc::tmem_alloc(&s_taddr, 512u);
   tc::tc_fence_before();
@@ -618,25 +628,58 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
         if (s_last) {
           __threadfence();
           auto part_of = [&](int k) { return p.slots + (size_t)(2 * (ta + k) + (k == 0 ? 1 : 0)) * p.slot_floats; };
-          for (int j = tid; j < rows * DH / 4; j += 256) {
-            const int rr = j / (DH / 4), ch = (j % (DH / 4)) * 4;
-            float M = -INFINITY;
+          // a thread per row: each part's factor, in the place of its maximum
+          if (tid < rows) {
+            float M = -INFINITY, L = 0.f;
 #pragma unroll 4
-            for (int k = 0; k < parts; ++k) M = fmaxf(M, __ldcg(part_of(k) + kRows * DH + rr));
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-            float L = 0.f;
+            for (int k = 0; k < parts; ++k) M = fmaxf(M, __ldcg(part_of(k) + kRows * DH + tid));
 #pragma unroll 4
             for (int k = 0; k < parts; ++k) {
-              const float* q = part_of(k);
-              const float mk = __ldcg(q + kRows * DH + rr), e = mk == -INFINITY ? 0.f : ex2(mk - M);
-              const float4 x = __ldcg(reinterpret_cast<const float4*>(q + (size_t)rr * DH + ch));
-              L += __ldcg(q + kRows * DH + kRows + rr) * e;
-              a.x += x.x * e;
-              a.y += x.y * e;
-              a.z += x.z * e;
-              a.w += x.w * e;
+              const float mk = __ldcg(part_of(k) + kRows * DH + tid);
+              L += mk == -INFINITY ? 0.f : __ldcg(part_of(k) + kRows * DH + kRows + tid) * ex2(mk - M);
             }
-            store_row<true>(p, w.r, w.hk, w.tile * kRows + rr, ch, a, L);
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll 4
+            for (int k = 0; k < parts; ++k) {
+              const float mk = __ldcg(part_of(k) + kRows * DH + tid);
+              __stcg(part_of(k) + kRows * DH + tid, mk == -INFINITY ? 0.f : ex2(mk - M) * inv);
+            }
+          }
+          asm volatile("bar.sync 1, 256;" ::: "memory");
+          // eight pieces of a thread at a time, so that their loads do not wait for one another
+          // (one at a time, a tile of four parts took 50 us)
+          constexpr int U = 8;
+          for (int j0 = tid; j0 < rows * DH / 4; j0 += 256 * U) {
+            float4 a[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) a[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < parts; ++k) {
+              const float* q = part_of(k);
+              float4 x[U];
+              float f[U];
+#pragma unroll
+              for (int u = 0; u < U; ++u) {
+                const int j = j0 + 256 * u;
+                f[u] = 0.f;
+                if (j < rows * DH / 4) {
+                  x[u] = __ldcg(reinterpret_cast<const float4*>(q) + j);
+                  f[u] = __ldcg(q + kRows * DH + j / (DH / 4));
+                }
+              }
+#pragma unroll
+              for (int u = 0; u < U; ++u)
+                if (j0 + 256 * u < rows * DH / 4) {
+                  a[u].x += x[u].x * f[u];
+                  a[u].y += x[u].y * f[u];
+                  a[u].z += x[u].z * f[u];
+                  a[u].w += x[u].w * f[u];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const int j = j0 + 256 * u;
+              if (j < rows * DH / 4) store_row<true>(p, w.r, w.hk, w.tile * kRows + j / (DH / 4), (j % (DH / 4)) * 4, a[u], 1.f);
+            }
           }
         }
         asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -653,17 +696,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
   }
 }
 
-bool prompt_takes(bool bf16, int64_t dh, int64_t rows) { return bf16 && dh <= 128 && rows > 64; }
+// More than 96 query rows a request and kv head, and 20 tiles at least over all: below that
+// k_kv8_attn_split is as fast or faster (32 / 8 heads, 6 K keys: 4 requests of 24 queries 67 us
+// against 70 here, of 128 queries 250 against 130; one request of 64 queries, 8 tiles, 51 against
+// 82; 32 requests of 32 queries 242 against 172).
+bool prompt_takes(bool bf16, int64_t dh, int64_t rows, int64_t all_rows) {
+  return bf16 && dh <= 128 && rows > 96 && all_rows >= 20 * kRows;
+}
+
 
 size_t prompt_slot_floats(int64_t dh) { return (size_t)kRows * (dh + 2); }
 
-wina_status_t launch_prompt(AttnParams& p, int64_t rows, cudaStream_t s) {
+wina_status_t launch_prompt(AttnParams& p, cudaStream_t s) {
   const int sms = device_sm_count();
   if (sms < 1) return WINA_ERR_CUDA;
   p.slot_floats = (int)prompt_slot_floats(p.c.dh);
   p.tiles = 0;
   p.tile_cost = 2;
-  (void)rows;
   const bool e4 = p.c.format == KV8_E4M3;
   void (*kern)(const AttnParams) = p.c.dh == 64 ? (e4 ? k_kv8_attn_prompt<true, 64> : k_kv8_attn_prompt<false, 64>)
                                                 : (e4 ? k_kv8_attn_prompt<true, 128> : k_kv8_attn_prompt<false, 128>);

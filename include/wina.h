@@ -518,8 +518,13 @@ wina_status_t kv8_read(const kv8_cache_t* cache, const int32_t* slots, int64_t T
  *   ws: device scratch of wina_workspace_size(WINA_OP_KV8_ATTENTION, dh, max_q * Hq / Hkv,
  *     0, B) bytes (see that function).
  *   A kv_len outside [0, width * page] or a cu_q that descends or leaves [0, T] is clamped
- *   and recorded as WINA_ERR_INVALID_ARG. 1 <= B <= 8192, Hq / Hkv <= 64, T <= 2^24.
- *   Deterministic: fixed-order sums throughout. */
+ *   and recorded as WINA_ERR_INVALID_ARG; so is a call that would read more than 2^37 keys,
+ *   which computes nothing. 1 <= B <= 8192, Hq / Hkv <= 64, T <= 2^24. out overlaps neither q
+ *   nor the pages. A wait inside the kernel is bounded (1 s; WINA_ERR_TIMEOUT).
+ *   Deterministic: fixed-order sums throughout, so the same call gives the same bits.
+ *   bf16: the weights are rounded to float16 with their value scales (11 bits down to 2^-19
+ *   of a row's largest), the queries and bytes are exact; float32: queries and weights are
+ *   held as two float16 parts (22 bits). e4m3 bytes are numbers (kv8_write stores no NaN). */
 wina_status_t kv8_attention(const kv8_cache_t* cache, const void* q, wina_dtype_t qdt, int64_t T, int64_t ld_q,
                             int64_t Hq, const int32_t* table, int64_t width, const int32_t* kv_len,
                             const int32_t* cu_q, int64_t B, int64_t max_q, float scale, int64_t window, float softcap,
