@@ -256,7 +256,7 @@ struct WriteParams {
 
 // One warp per (run of rows in one page, head, keys or values): the rows' largest magnitude,
 // the scale, the bytes. DH / 8 lanes hold a row, eight channels each, so a pass over up to
-// kRows rows has all its 16-byte loads in flight; a run longer than that is read twice, the
+// IT * RPP rows has all its 16-byte loads in flight; a run longer than that is read twice, the
 // second time from L1/L2. Bound by HBM for prompts (each element read once, one byte
 // written), by latency for single tokens. Four CTAs of 64 registers share an SM: with more rows
 // in registers, or the runs' lengths found beforehand, 15500 bf16 rows of 8 x 128 in pages of 32

@@ -59,7 +59,7 @@ __device__ __forceinline__ uint32_t staged(int r, int c) {
   else return (c >> 3) * 2048 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
-// The variants' sizes. The registers set the number of consumer warps (a tile's sums and
+// The variants' sizes. The registers set the number of warps (a tile's sums and
 // queries: 16 rows, or rows of 256, or queries in two parts take the most); the shared memory
 // the depth of their rings.
 template <bool BF16, int DH, int NT>
@@ -67,7 +67,7 @@ struct SplitShape {
   static constexpr int CH = DH == 256 ? 16 : 32;          // keys of a chunk
   static constexpr int R = 8 * NT;                        // query rows of a tile
   static constexpr int STAGE = 2 * CH * DH;               // bytes of a chunk, keys and values
-  static constexpr int NCW = NT * DH == 256 ? 8 : 12;     // warps: 168 or 255 registers a thread
+  static constexpr int NCW = NT * DH == 256 ? 8 : 12;     // warps, of 255 or 168 registers a thread
   static constexpr int THREADS = 32 * NCW;
   static constexpr int S = DH == 64 ? 4 : NCW == 8 ? 3 : 2;  // chunks of a warp's ring
   static constexpr int RPR = DH == 256 ? 2 : 4;           // rows joined at a time
@@ -75,13 +75,14 @@ struct SplitShape {
   static constexpr size_t SMEM = (size_t)NCW * S * STAGE + MERGE;
 };
 
-// One CTA per SM: consumer warps, and one warp whose lane w feeds consumer warp w. The work
-// (tiles of 8 NT query rows of one request and kv head, times the chunks of CH keys they see)
-// is a line cut into equal parts, one for each team, so that one long sequence fills the GPU
-// and a ragged batch is balanced. A team is a whole CTA, whose warps take a tile's chunks in
-// turn (few tiles), or one warp (many tiles, whose fixed costs then run side by side). Each
-// warp has its own ring of chunks, filled by tensor copies of 16 keys; the feeding lane runs on
-// across tiles, so loads stay in flight while tiles are joined.
+// One CTA per SM. The work (tiles of 8 NT query rows of one request and kv head, times the
+// chunks of CH keys they see) is a line cut into equal parts, one for each team, so that one long
+// sequence fills the GPU and a ragged batch is balanced. A team is a whole CTA, whose warps take
+// a tile's chunks in turn (few tiles), or one warp (many tiles, whose fixed costs then run side by
+// side). Each warp copies its own chunks into its own ring (cp.async, 16 bytes a lane; places
+// outside the tile's keys become zeros and are not read), running ahead across tiles, so that
+// loads stay in flight while tiles are joined. (A warp that feeds the others by tensor copies was
+// slower: a copy of 16 x 128 bytes takes it 80 to 116 cycles.)
 //
 // Per chunk, with keys as the rows of the matrix instruction, so that 8 query rows cost half
 // of what 16 do:
@@ -98,7 +99,8 @@ struct SplitShape {
 // from the first's (2-norm errors at 9 K keys: 0.4e-6 to 0.9e-6, and 0.7e-6 to 3.2e-6 without, for
 // 2 % of the time, or 15 % with 16 rows).
 // The bytes' conversion and the softmax, some 420 instructions a chunk of 32 keys in one
-// dependent stream, are what a warp spends its time on; eleven warps hide its latency.
+// dependent stream, are what a warp spends its time on; twelve warps hide its latency (64 long
+// contexts, 1.3 GB: 207 us, 6.3 TB/s; 264 us with eight warps).
 // A team's warps' (max, sum, O) are joined in shared memory in warp order; a tile cut by a
 // part's end is left in the workspace, and the last team of that tile to arrive joins the
 // parts in order. No team waits for another.
@@ -755,11 +757,11 @@ extern "C" wina_status_t kv8_attention(const kv8_cache_t* cache, const void* q, 
   if (!cu_q && (T != B || max_q != 1)) return WINA_ERR_INVALID_ARG;
   if (ld_q < Hq * cache->dh || ld_q > INT32_MAX || ld_q * elem_size(qdt) % 16) return WINA_ERR_INVALID_ARG;
   if (!aligned(status_dev, 4)) return WINA_ERR_INVALID_ARG;
+  if (T == 0) return WINA_OK;
   if (!q || !table || !kv_len || !out || !ws || !aligned(q, 16) || !aligned(out, 16) || !aligned(ws, 16) ||
       !aligned(table, 4) || !aligned(kv_len, 4) || !aligned(cu_q, 4))
     return WINA_ERR_INVALID_ARG;
   if (ws_bytes < kv8_attention_ws_size(cache->dh, max_q * (Hq / cache->heads))) return WINA_ERR_WORKSPACE;
-  if (T == 0) return WINA_OK;
   AttnParams p;
   p.c = *cache;
   p.q = q;

@@ -466,6 +466,8 @@ typedef struct {
  * seq_len < 0 or more tokens than width * page is left out the same way (kv_len: seq_len
  * clamped to the table) with WINA_ERR_INVALID_ARG, as is an *n_free outside [0, cells]
  * (clamped). Pages pushed past the last cell are lost, with WINA_ERR_CAPACITY.
+ * All pages of an ended request go back, so its table must not hold a page that another request
+ * still uses.
  * The outputs other than the stack's cells depend on the inputs alone, so with separate
  * kv_len and n_free_out the call can be repeated.
  *   1 <= B <= 8192; tokens >= 0; width >= 1, width * page < 2^31; cells >= 1. */

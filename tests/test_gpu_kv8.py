@@ -386,6 +386,24 @@ def test_attention_window_softcap_scale(window, softcap, scale, dtype, pad):
         check_attention(out, m, q, table, kv, cu, dtype, **args)
 
 
+def test_calls_without_tokens():
+    """A step in which no request brings a token (and one in which all end)."""
+    t = torch()
+    m, q, table, cu = attention_case(30, [20, 30], [1, 1], 4, 2, 64, 16, "int8", "bf16")
+    lens, none = dev_i32(np.array([20, 30])), dev_i32(np.zeros(2))
+    r = W.kv8_plan(lens, none, dev_i32(table), dev_i32(np.arange(4)), dev_i32(np.array([4])), 16, 0)
+    assert host(r[0]).tolist() == [20, 30] and host(r[1]).tolist() == [0, 0, 0] and r[2].numel() == 0
+    r = W.kv8_plan(lens, none - 1, dev_i32(table), dev_i32(np.arange(9)), dev_i32(np.array([4])), 16, 0)
+    assert host(r[0]).tolist() == [0, 0] and int(host(r[4])[0]) == 4 + 2 + 2
+    assert W.kv8_attention(m.c, q[:0], dev_i32(table), lens, cu_q=r[1], max_q=7).shape == (0, 4, 64)
+    W.kv8_write(m.c, q[:0, :2], q[:0, 2:], r[2])
+    assert W.kv8_read(m.c, r[2])[1].shape == (0, 2, 64)
+    # rows, but no request has any: left as they were
+    out = t.full((3, 4, 64), 7.0, dtype=t.bfloat16, device="cuda")
+    W.kv8_attention(m.c, t.ones_like(out), dev_i32(table), lens, cu_q=r[1], max_q=1, out=out)
+    assert (f64(out) == 7.0).all()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_attention_leaves_rows_behind_the_last_request(dtype):
     for ql, pad in (([1, 1, 1], 5), ([3, 1, 2], 5), ([150, 1, 40], 5), ([150, 1, 40], 900)):
