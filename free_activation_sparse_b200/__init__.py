@@ -119,9 +119,15 @@ def declared_symbols() -> list[str]:
 # ------------------------------------------------------------------------------------
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dt(t) -> int:
@@ -553,12 +559,13 @@ class Kv8Cache:
     def _struct(self) -> _Kv8T:
         torch = _torch()
         k, v = self.k, self.v
-        fmt = {torch.int8: KV8_INT8, torch.float8_e4m3fn: KV8_E4M3}.get(k.dtype)
-        if fmt is None or v.dtype != k.dtype:
+        dt = k.dtype
+        if v.dtype is not dt or (dt is not torch.int8 and dt is not torch.float8_e4m3fn):
             raise TypeError("k and v must both be int8 or both float8_e4m3fn")
-        if k.dim() != 4 or v.shape != k.shape:
+        fmt, shape = KV8_INT8 if dt is torch.int8 else KV8_E4M3, k.shape
+        if len(shape) != 4 or v.shape != shape:
             raise ValueError("k and v must be [n_pages][heads][page][dh], of one shape")
-        n, h, page, dh = k.shape
+        n, h, page, dh = shape
         dev = k.device
         for t in (self.k_scale, self.v_scale):
             if t.dtype is not torch.float32:

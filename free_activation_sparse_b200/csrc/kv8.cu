@@ -152,37 +152,42 @@ __global__ void __launch_bounds__(kPlanT) k_kv8_plan(PlanParams p) {
   if (want_top > p.cells && blockIdx.x == 0 && tid == 0) record_status(p.status, WINA_ERR_CAPACITY);
   // whether request b gets its places; its tokens' prefix sums are exact if it does
   auto served = [&](int b) { return seq[b] >= 0 && need[b + 1] <= top && tok[b + 1] <= p.tokens; };
-  // the r-th page pushed
-  auto pushed_page = [&](int r) {
+  // where the r-th page pushed, and the j-th page popped, are read
+  auto pushed_at = [&](int r) -> const int32_t* {
     const int b = last_at_most(back, B, r);
-    return p.table[(int64_t)b * p.width + (r - back[b])];
+    return p.table + (int64_t)b * p.width + (r - back[b]);
   };
-  // the j-th page popped
-  auto popped_page = [&](int j) {
+  auto popped_at = [&](int j) {
     const int e = top - 1 - j;
-    return e < n_free ? p.free_pages[e] : pushed_page(e - n_free);
+    return e < n_free ? p.free_pages + e : pushed_at(e - n_free);
   };
   const int ctas = gridDim.x, rank = blockIdx.x;
   // tokens, four to a thread
   for (int64_t t0 = 4 * ((int64_t)rank * kPlanT + tid); t0 < p.tokens; t0 += 4LL * ctas * kPlanT) {
-    int sl[4], ps[4];
+    int sl[4], ps[4], pg[4];
+    const int32_t* at[4];
     int b = B;
     if (t0 < tok[B]) b = last_at_most(tok, B, (int)t0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 4; ++i) {  // first where the pages are read, then all four at once
       const int64_t t = t0 + i;
-      sl[i] = -1;
+      at[i] = nullptr;
       ps[i] = 0;
       if (t >= p.tokens) continue;
       while (b < B && t >= tok[b + 1]) ++b;
       if (b < B && served(b)) {
         const int pos = seq[b] + (int)t - tok[b], pi = pos >> p.shift, have = (seq[b] + page - 1) >> p.shift;
-        const int pg = pi < have ? p.table[(int64_t)b * p.width + pi] : popped_page(need[b] + pi - have);
-        if (pg >= 0 && pg <= (0x7fffffff >> p.shift)) {
-          sl[i] = (pg << p.shift) | (pos & (page - 1));
-          ps[i] = pos;
-        }
+        at[i] = pi < have ? p.table + (int64_t)b * p.width + pi : popped_at(need[b] + pi - have);
+        ps[i] = pos;
       }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pg[i] = at[i] ? *at[i] : -1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool ok = pg[i] >= 0 && pg[i] <= (0x7fffffff >> p.shift);
+      sl[i] = ok ? (pg[i] << p.shift) | (ps[i] & (page - 1)) : -1;
+      if (!ok) ps[i] = 0;
     }
     if (t0 + 4 <= p.tokens) {
       *reinterpret_cast<int4*>(p.slots + t0) = make_int4(sl[0], sl[1], sl[2], sl[3]);
@@ -199,16 +204,17 @@ __global__ void __launch_bounds__(kPlanT) k_kv8_plan(PlanParams p) {
     const int b = last_at_most(need, B, j);
     if (served(b)) {
       const int have = (seq[b] + page - 1) >> p.shift;
-      p.table[(int64_t)b * p.width + have + (j - need[b])] = popped_page(j);
+      p.table[(int64_t)b * p.width + have + (j - need[b])] = *popped_at(j);
     }
   }
-  for (int r0 = rank * kPlanT + tid; r0 < pushed; r0 += 4 * ctas * kPlanT) {
+  // (the last threads first: the first ones have the tokens)
+  for (int r0 = (ctas - 1 - rank) * kPlanT + (kPlanT - 1 - tid); r0 < pushed; r0 += 4 * ctas * kPlanT) {
     // four at a time: their searches and loads do not wait for one another
     int pg[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int r = r0 + u * ctas * kPlanT;
-      pg[u] = r < pushed ? pushed_page(r) : 0;
+      pg[u] = r < pushed ? *pushed_at(r) : 0;
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {

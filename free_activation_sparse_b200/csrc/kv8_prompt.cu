@@ -8,6 +8,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "kv8_attn.cuh"
 
@@ -716,6 +717,16 @@ wina_status_t launch_prompt(AttnParams& p, cudaStream_t s) {
   const bool e4 = p.c.format == KV8_E4M3;
   void (*kern)(const AttnParams) = p.c.dh == 64 ? (e4 ? k_kv8_attn_prompt<true, 64> : k_kv8_attn_prompt<false, 64>)
                                                 : (e4 ? k_kv8_attn_prompt<true, 128> : k_kv8_attn_prompt<false, 128>);
+  // the register split draws on what the kernel is launched with: never launch it with less
+  static std::atomic<bool> checked[4];
+  std::atomic<bool>& seen = checked[(p.c.dh == 64 ? 2 : 0) + (e4 ? 1 : 0)];
+  if (!seen.load(std::memory_order_relaxed)) {
+    cudaFuncAttributes a;
+    const cudaError_t e = cudaFuncGetAttributes(&a, (const void*)kern);
+    if (e != cudaSuccess) return cuda_status(e);
+    if (a.numRegs < kLaunchRegs) return WINA_ERR_CUDA;
+    seen.store(true, std::memory_order_relaxed);
+  }
   const size_t smem = (p.c.dh == 64 ? PromptShape<64>::SMEM : PromptShape<128>::SMEM) + round_up((size_t)pre_entries(p.B) * 4, 16);
   return cuda_status(launch_kernel(kern, dim3((unsigned)std::min(sms, kMaxCtas)), dim3(kThreads), smem, s, false, p));
 }
