@@ -149,13 +149,8 @@ __global__ void __launch_bounds__(SplitShape<BF16, DH, NT>::THREADS, 1)
   const unsigned long long u0 = team_start(C, nc, team), u1 = team_start(C, nc, team + 1);
 
   using W = Walk<R, CH>;
-  // the chunks [from, to) of a tile that this team has (none where its part of the line ends in
-  // the tile's fixed cost); this warp's are from + member, + TEAM, ...
-  auto part = [&](const W& w, int& from, int& to) {
-    const unsigned long long first = w.at + p.tile_cost, end = w.at + w.len(p);
-    from = w.s.c0 + (int)(u0 > first ? u0 - first : 0);
-    to = u1 >= end ? w.s.c1 : u1 > first ? w.s.c0 + (int)(u1 - first) : w.s.c0;
-  };
+  // of a team's chunks [from, to) this warp's are from + member, + TEAM, ...
+  auto part = [&](const W& w, int& from, int& to) { w.part(p, u0, u1, from, to); };
   W w;  // the tile being computed
   w.locate(p, pre, u0);
 

@@ -164,6 +164,14 @@ struct Walk {
   unsigned long long at;  // the line's units before this tile
 
   __device__ __forceinline__ unsigned len(const AttnParams& p) const { return s.len(p); }
+  // The chunks [from, to) of the tile that the team of units [u0, u1) has; none where its part of
+  // the line ends in the tile's fixed cost, and none of a tile that sees no key, wherever the
+  // part ends in it.
+  __device__ __forceinline__ void part(const AttnParams& p, unsigned long long u0, unsigned long long u1, int& from, int& to) const {
+    const unsigned long long first = at + p.tile_cost, end = at + len(p);
+    from = s.c0 + (int)(u0 > first ? u0 - first : 0);
+    to = u1 >= end ? s.c1 : u1 > first ? min(s.c1, s.c0 + (int)(u1 - first)) : s.c0;
+  }
   // whether the tile's rows only get zeros, and the team of units [u0, u1) is to write them
   __device__ __forceinline__ bool empty_of(unsigned long long u0, unsigned long long u1) const {
     return s.c0 == s.c1 && at >= u0 && at < u1;

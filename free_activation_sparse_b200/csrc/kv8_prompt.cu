@@ -210,11 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
   const unsigned long long u0 = team_start(C, nc, team), u1 = team_start(C, nc, team + 1);
 
   using W = Walk<kRows, kKeys>;
-  auto part = [&](const W& w, int& from, int& to) {
-    const unsigned long long first = w.at + p.tile_cost, end = w.at + w.len(p);
-    from = w.s.c0 + (int)(u0 > first ? u0 - first : 0);
-    to = u1 >= end ? w.s.c1 : u1 > first ? w.s.c0 + (int)(u1 - first) : w.s.c0;
-  };
+  auto part = [&](const W& w, int& from, int& to) { w.part(p, u0, u1, from, to); };
   // A wait that ran out (1 s) makes every later wait of the CTA return at once; all loops end by
   // their counts.
   auto wait = [&](uint64_t* bar, uint32_t parity) {

@@ -704,3 +704,72 @@ def test_double_sparsity_is_calibrated_from_the_cache():
         assert host(C)[g].tolist() == O.ds_calibrate_channels(rows64[:, g], 8).tolist()
     lab = host(W.ds_label_build(K, seq, C))
     assert np.array_equal(lab[0, 1, :60], rows64[:, 1][:, host(C)[1]])
+
+
+# ------------------------------------------------------------------------------------
+# calls that go past what the tests above reach
+# ------------------------------------------------------------------------------------
+
+
+# Requests with fewer keys than queries, so that whole tiles of query rows see no key, in every
+# kernel and kind of team: kv length, queries, requests, hq, hkv, dh, rows behind the last request.
+BLIND = [(100, 2048, 1, 32, 8, 128, 0), (5, 300, 1, 32, 8, 128, 0), (5, 300, 3, 8, 8, 64, 5200),  # tensor-core kernel
+         (20, 64, 1, 8, 8, 128, 0), (20, 64, 1, 4, 2, 256, 0), (5, 60, 1, 8, 2, 64, 0), (100, 300, 1, 4, 2, 256, 0),  # CTAs
+         (5, 300, 1, 16, 8, 128, 0), (5, 300, 1, 32, 8, 64, 0), (30, 200, 4, 8, 4, 256, 0)]  # one-warp teams
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kv,n,B,hq,hkv,dh,pad", BLIND)
+def test_attention_tiles_that_see_no_key(kv, n, B, hq, hkv, dh, pad, dtype):
+    """Their rows are zeros, whatever lay in `out`, and the workspace is left as a call has to
+    find it: a call whose tiles are cut, on the same workspace, gives what it gives on a new one."""
+    t = torch()
+    m, q, table, cu = attention_case(kv + n, [kv] * B, [n] * B, hq, hkv, dh, 16, "int8", dtype, pad=pad)
+    ws = W.Workspace(W.OP_KV8_ATTENTION, dh, n * hq // hkv, 0, B)
+    out = t.full(tuple(q.shape), 7.0, dtype=q.dtype, device="cuda")
+    st = status_word()
+    args = dict(cu_q=dev_i32(cu), max_q=n)
+    W.kv8_attention(m.c, q, dev_i32(table), dev_i32(np.array([kv] * B)), ws=ws, out=out, status=st, **args)
+    assert int(host(st)[0]) == 0
+    for b in range(B):
+        assert not f64(out)[cu[b]:cu[b + 1] - kv].any(), b
+    check_attention(out, m, q, table, [kv] * B, cu, dtype)
+    assert (f64(out)[cu[-1]:] == 7.0).all()
+    assert not ws.buf[:160 * 12 * 4].any()  # the teams' arrival counters, which lead the workspace
+    m2, q2, table2, cu2 = attention_case(n, [3000] * B, [min(n, 200)] * B, hq, hkv, dh, 16, "int8", dtype, pad=pad)
+    args = dict(cu_q=dev_i32(cu2), max_q=n)
+    want = W.kv8_attention(m2.c, q2, dev_i32(table2), dev_i32(np.array([3000] * B)), **args)
+    for _ in range(2):
+        got = W.kv8_attention(m2.c, q2, dev_i32(table2), dev_i32(np.array([3000] * B)), ws=ws, **args)
+        assert t.equal(got, want)
+
+
+def test_serving_step_that_runs_out_of_pages():
+    """kv8_plan leaves requests out: their lengths stay, their new tokens keep their rows. The
+    others' rows are right, and so are the next step's on the same workspace."""
+    t = torch()
+    rng = np.random.default_rng(8)
+    B, hq, hkv, dh, page, max_q = 3, 8, 2, 64, 16, 600
+    s = Server(B, B * max_q, hq, hkv, dh, page, 50, 50, "int8", "bf16", max_q)
+    k = v = (np.zeros((50, hkv, page, dh)), np.zeros((50, hkv)))
+    ref = dict(len=np.zeros(B, dtype=np.int64), table=host(s.table).astype(np.int64), free=host(s.free).astype(np.int64), n=50)
+    # the second step finds 9 pages free: the last request's 600 tokens do not fit behind its 40
+    for new, short in (([400, 200, 40], False), ([2, 1, 600], True), ([3, 1, 100], False)):
+        new = np.array(new)
+        x, xf = rows(rng, tuple(s.qkv.shape), "bf16")
+        s.qkv.copy_(x)
+        s.new.copy_(dev_i32(new))
+        s.out.fill_(7.0)
+        s.status.zero_()
+        s.step()
+        t.cuda.synchronize()
+        p = O.kv8_plan(ref["len"], new, ref["table"], ref["free"], ref["n"], page, B * max_q)
+        assert p["short"] == short and int(host(s.status)[0]) == (W.ERR_CAPACITY if short else 0)
+        assert np.array_equal(host(s.len), p["kv_len"]) and np.array_equal(host(s.cu), p["cu_q"])
+        k = O.kv8_write(*k, xf[:, hq:hq + hkv], p["slots"], page, "int8")
+        v = O.kv8_write(*v, xf[:, hq + hkv:], p["slots"], page, "int8")
+        m = Mirror.__new__(Mirror)
+        m.page, m.k, m.v = page, k, v
+        check_attention(s.out, m, s.qkv[:, :hq], p["table"], p["kv_len"].tolist(), p["cu_q"], "bf16")
+        assert (f64(s.out)[p["cu_q"][-1]:] == 7.0).all()
+        ref = dict(len=p["kv_len"], table=p["table"], free=p["free_pages"], n=p["n_free"])
