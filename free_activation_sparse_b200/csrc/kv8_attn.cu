@@ -598,7 +598,9 @@ __global__ void __launch_bounds__(SplitShape<BF16, DH, NT>::THREADS, 1)
 #pragma unroll
         for (int k = 0; k < NCW; ++k) {
           const float mk = s_m[k][rr], f = mk == -INFINITY ? 0.f : ex2(mk - M);
-          if (f == 0.f) continue;  // a warp without keys, or without weight
+          // a warp without keys (not one whose scores are all NaN: fmaxf leaves its maximum at -inf
+          // too, and its sums have to arrive)
+          if (s_l[k][rr] == 0.f) continue;
           const float4 x = *reinterpret_cast<const float4*>(mbuf + ((size_t)k * RPR + row) * DH + ch);
           L += s_l[k][rr] * f;
           a.x += x.x * f;

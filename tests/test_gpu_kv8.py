@@ -773,3 +773,41 @@ def test_serving_step_that_runs_out_of_pages():
         check_attention(s.out, m, s.qkv[:, :hq], p["table"], p["kv_len"].tolist(), p["cu_q"], "bf16")
         assert (f64(s.out)[p["cu_q"][-1]:] == 7.0).all()
         ref = dict(len=p["kv_len"], table=p["table"], free=p["free_pages"], n=p["n_free"])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("page,dh,kv,ql,hq,hkv,pad", [
+    (16, 64, [10], [1], 4, 2, 0), (16, 256, [100], [1], 4, 2, 0), (32, 128, [10], [1], 8, 2, 0), (32, 64, [100], [3], 4, 2, 0),
+    (64, 128, [100], [1], 2, 2, 0), (128, 256, [700], [2], 8, 2, 0), (128, 64, [700], [1], 4, 2, 0),
+    (32, 128, [900] * 64, [1] * 64, 16, 8, 0), (64, 64, [130] * 64, [1] * 64, 16, 8, 0), (64, 256, [130] * 64, [1] * 64, 16, 8, 0),
+    (64, 128, [300, 400], [100, 130], 4, 2, 5200), (128, 64, [300, 400], [100, 130], 4, 2, 5200)])
+def test_attention_carries_nan(page, dh, kv, ql, hq, hkv, pad, dtype):
+    """A page whose key scale is NaN (kv8_write met an infinity or a NaN there) gives NaN to every
+    row that sees a key of it, wherever the page lies among the kernels' chunks and warps; a query
+    with a NaN or an infinity gives NaN to its own row of that head."""
+    m, q, table, cu = attention_case(77, kv, ql, hq, hkv, dh, page, "int8", dtype, pad=pad)
+    args = (dev_i32(table), dev_i32(np.array(kv)))
+    more = dict(cu_q=dev_i32(cu), max_q=max(ql))
+    base = f64(W.kv8_attention(m.c, q, *args, **more))
+    G, b = hq // hkv, len(kv) - 1
+    assert np.isfinite(base).all()
+    pages = -(-kv[b] // page)
+    for at in sorted({0, pages // 2, pages - 1}):
+        keep = m.c.k_scale.clone()
+        m.c.k_scale[int(table[b, at]), 1] = float("nan")
+        out = f64(W.kv8_attention(m.c, q, *args, **more))
+        m.c.k_scale.copy_(keep)
+        want = np.zeros(out.shape, dtype=bool)
+        for i in range(ql[b]):
+            want[cu[b] + i, G:2 * G] = kv[b] - ql[b] + i >= at * page
+        assert np.array_equal(np.isnan(out), want), at
+        assert np.array_equal(out[~want], base[~want])
+    for bad in (float("nan"), float("inf")):
+        q2 = q.clone()
+        row, head = int(cu[b]) + ql[b] // 2, hq - 1
+        q2[row, head, 3] = bad
+        out = f64(W.kv8_attention(m.c, q2, *args, **more))
+        want = np.zeros(out.shape, dtype=bool)
+        want[row, head] = True
+        assert np.array_equal(np.isnan(out), want), bad
+        assert np.array_equal(out[~want], base[~want])
