@@ -382,6 +382,8 @@ __global__ void __launch_bounds__(SplitShape<BF16, DH, NT>::THREADS, 1)
       for (int u = 0; u < MT; ++u) {
         ks[u] = s_meta[warp][slot][u];
         vs[u] = s_meta[warp][slot][MT + u];
+        // values that no scale holds: the scores say so, since a weight may be too small to
+        if (!(fabsf(vs[u]) < INFINITY)) ks[u] = __uint_as_float(0x7fc00000u);
       }
       const uint32_t bad = s_bad[warp][slot];
       const int key0 = c * CH;

@@ -811,3 +811,27 @@ def test_attention_carries_nan(page, dh, kv, ql, hq, hkv, pad, dtype):
         want[row, head] = True
         assert np.array_equal(np.isnan(out), want), bad
         assert np.array_equal(out[~want], base[~want])
+
+
+@PADS
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B", [1, 80])
+def test_attention_nan_values_reach_rows_that_hardly_weigh_them(B, dtype, pad):
+    """A page whose value scale is NaN, its keys' weights far below float32's smallest number: as
+    with the values themselves, 0 * NaN is NaN."""
+    kv, ql = [300] * B, [2] * (B - 1) + [130]
+    m, q, table, cu = attention_case(78, kv, ql, 8, 4, 64, 16, "int8", dtype, pad=pad)
+    m.c.k_scale.mul_(256.0)  # scores apart by hundreds
+    args = (dev_i32(table), dev_i32(np.array(kv)))
+    more = dict(cu_q=dev_i32(cu), max_q=130)
+    base = f64(W.kv8_attention(m.c, q, *args, **more))
+    assert np.isfinite(base).all()
+    for b in {0, B - 1}:
+        for at in (0, 3):
+            keep = m.c.v_scale.clone()
+            m.c.v_scale[int(table[b, at]), 2] = float("nan")
+            out = f64(W.kv8_attention(m.c, q, *args, **more))
+            m.c.v_scale.copy_(keep)
+            assert np.isnan(out[cu[b]:cu[b + 1], 4:6]).all()
+            out[cu[b]:cu[b + 1], 4:6] = base[cu[b]:cu[b + 1], 4:6]
+            assert np.array_equal(out, base)
