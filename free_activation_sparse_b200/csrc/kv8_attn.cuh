@@ -124,18 +124,52 @@ __device__ __forceinline__ unsigned long long req_cost(const AttnParams& p, cons
   return c;
 }
 
+// x + y, 2^32 - 1 where the sum passes 32 bits.
+__device__ __forceinline__ uint32_t add_sat(uint32_t x, uint32_t y) {
+  const uint32_t s = x + y;
+  return s < x ? 0xffffffffu : s;
+}
+
+// block_excl_scan with sums that stay at 2^32 - 1 once they reach it (the prefixes then mean nothing).
+template <int NTHR>
+__device__ __forceinline__ uint32_t block_excl_scan_sat(uint32_t v, uint32_t* red, uint32_t* total) {
+  constexpr int NW = NTHR / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x = add_sat(x, y);
+  }
+  if (lane == 31) red[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    uint32_t w = lane < NW ? red[lane] : 0u;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w = add_sat(w, y);
+    }
+    if (lane < NW) red[lane] = w;  // inclusive over warps
+  }
+  __syncthreads();
+  const uint32_t before = warp ? red[warp - 1] : 0u;
+  *total = red[NW - 1];
+  __syncthreads();
+  return before + x - v;
+}
+
 // Prefix sums of req_cost before every fourth request, in shared memory (pre[ceil(B / 4)] the
-// total). Returns false where they pass 32 bits (more than 2^37 keys read: no cache is that
-// large).
+// total). Returns false for a call that no cache's attention needs and that would run for
+// minutes to hours: 2^32 units or more for one kv head (the sums are 32 bits wide), or 2^36
+// over all heads (so that a team's chunks can be counted in 31 bits).
 constexpr int kPreStep = 4;
 __host__ __device__ constexpr int pre_entries(int B) { return (B + kPreStep - 1) / kPreStep + 1; }
 
 template <int NTHR, int R, int CH>
 __device__ bool cost_prefix(const AttnParams& p, uint32_t* pre, uint32_t* red) {
-  unsigned long long run = 0;
-  __shared__ int s_over;
-  if (threadIdx.x == 0) s_over = 0;
-  __syncthreads();
+  unsigned long long run = 0;  // the same in all threads
+  bool fits = true;
   for (int b0 = 0; b0 < p.B; b0 += NTHR) {
     const int b = b0 + threadIdx.x;
     unsigned long long c = 0;
@@ -143,16 +177,15 @@ __device__ bool cost_prefix(const AttnParams& p, uint32_t* pre, uint32_t* red) {
       c = req_cost<R, CH>(p, load_req(p, b));
       if (blockIdx.x == 0 && bad_req(p, b)) record_status(p.status, WINA_ERR_INVALID_ARG);
     }
-    if (c > 0xffffffffu / NTHR) s_over = 1;  // then the block's sum fits 32 bits below
     uint32_t total;
-    const uint32_t ex = block_excl_scan<NTHR>((uint32_t)min(c, (unsigned long long)(0xffffffffu / NTHR)), red, &total);
+    const uint32_t ex = block_excl_scan_sat<NTHR>((uint32_t)min(c, 0xffffffffull), red, &total);
     if (b < p.B && b % kPreStep == 0) pre[b / kPreStep] = (uint32_t)run + ex;
     run += total;
-    if (run > 0xffffffffu) s_over = 1;
+    fits = fits && total != 0xffffffffu;
   }
   if (threadIdx.x == 0) pre[pre_entries(p.B) - 1] = (uint32_t)run;
   __syncthreads();
-  return s_over == 0;
+  return fits && run <= 0xffffffffu && run * p.c.heads < (1ull << 36);
 }
 
 // A walk over tiles: requests in order, in each the kv heads, in each the row tiles.

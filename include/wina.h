@@ -520,8 +520,10 @@ wina_status_t kv8_read(const kv8_cache_t* cache, const int32_t* slots, int64_t T
  *   ws: device scratch of wina_workspace_size(WINA_OP_KV8_ATTENTION, dh, max_q * Hq / Hkv,
  *     0, B) bytes (see that function).
  *   A kv_len outside [0, width * page] or a cu_q that descends or leaves [0, T] is clamped
- *   and recorded as WINA_ERR_INVALID_ARG; so is a call that would read more than 2^37 keys,
- *   which computes nothing. 1 <= B <= 8192, Hq / Hkv <= 64, T <= 2^24. out overlaps neither q
+ *   and recorded as WINA_ERR_INVALID_ARG. The keys are read in pieces of 16 (dh 256), 32 or
+ *   128, once for each tile of 8 to 256 query rows of a key/value head; a call that comes to
+ *   2^32 pieces for one head, or 2^36 over all (a tile counts as up to 32 more), computes
+ *   nothing and records WINA_ERR_INVALID_ARG. 1 <= B <= 8192, Hq / Hkv <= 64, T <= 2^24. out overlaps neither q
  *   nor the pages. A wait inside the kernel is bounded (1 s; WINA_ERR_TIMEOUT).
  *   Deterministic: fixed-order sums throughout, so the same call gives the same bits.
  *   bf16: the weights are rounded to float16 with their value scales (11 bits down to 2^-19

@@ -835,3 +835,32 @@ def test_attention_nan_values_reach_rows_that_hardly_weigh_them(B, dtype, pad):
             assert np.isnan(out[cu[b]:cu[b + 1], 4:6]).all()
             out[cu[b]:cu[b + 1], 4:6] = base[cu[b]:cu[b + 1], 4:6]
             assert np.array_equal(out, base)
+
+
+@pytest.mark.parametrize("dtype,dh,hq,n,kv", [("bf16", 256, 8, 4096, 71000), ("f32", 256, 8, 4096, 71000), ("f32", 64, 16, 3000, 140000)])
+def test_attention_long_chunk_over_a_long_context(dtype, dh, hq, n, kv):
+    """One request with more pieces of keys than 2^32 over a CTA's threads. Sampled rows."""
+    m, q, table, cu = attention_case(31, [kv], [n], hq, 1, dh, 128, "int8", dtype)
+    st = status_word()
+    out = torch().full(tuple(q.shape), 7.0, dtype=q.dtype, device="cuda")
+    W.kv8_attention(m.c, q, dev_i32(table), dev_i32(np.array([kv])), cu_q=dev_i32(cu), max_q=n, out=out, status=st)
+    assert int(host(st)[0]) == 0
+    K, V = cached(m, table, 0, kv)
+    half = 2.0 ** -8 + 2.0 ** -11 if dtype == "bf16" else 1e-5
+    for i in (0, 1, n // 2, n - 1):
+        want, _, _ = O.kv8_attention(f64(q[i:i + 1]), K[:kv - n + i + 1], V[:kv - n + i + 1])
+        assert rel_l2(f64(out[i:i + 1]), want) <= half
+
+
+def test_attention_that_would_run_for_hours_is_refused():
+    """A table that names one page 2^23 times over: 2^34 pieces of keys for the head (2^33 for
+    the tensor-core kernel), and with fewer rows but 1024 heads 2^37 over all. Nothing is computed."""
+    t = torch()
+    table = t.zeros((1, (1 << 30) // 128), dtype=t.int32, device="cuda")
+    for dtype, dh, heads, hq, n, kv in (("bf16", 256, 1, 64, 32, 1 << 30), ("f32", 256, 1024, 1024, 9, 1 << 30),
+                                        ("bf16", 64, 1, 64, 4096, 1 << 30)):
+        c = W.kv8_cache(1, heads, 128, dh)
+        q, out = (t.full((n, hq, dh), 7.0, dtype=dtype_of(dtype), device="cuda") for _ in range(2))
+        st = status_word()
+        W.kv8_attention(c, q, table, dev_i32(np.array([kv])), cu_q=dev_i32(np.array([0, n])), max_q=n, out=out, status=st)
+        assert int(host(st)[0]) == W.ERR_INVALID_ARG and bool((out == 7.0).all())
