@@ -101,7 +101,7 @@ struct SplitShape {
 // The bytes' conversion and the softmax, some 420 instructions a chunk of 32 keys in one
 // dependent stream, are what a warp spends its time on; twelve warps hide its latency (64 long
 // contexts, 1.3 GB: 207 us, 6.3 TB/s; 264 us with eight warps).
-// A team's warps' (max, sum, O) are joined in shared memory in warp order; a tile cut by a
+// A team's warps' (max, sum, O / sum) are joined in shared memory in warp order; a tile cut by a
 // part's end is left in the workspace, and the last team of that tile to arrive joins the
 // parts in order. No team waits for another.
 template <bool BF16, bool E4M3, int DH, int NT, bool WARPS>
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(SplitShape<BF16, DH, NT>::THREADS, 1)
     if (from >= to) {
       if (w.empty_of(u0, u1))
         for (int i = member * 32 + lane; i < rows * DH / 4; i += 32 * TEAM)
-          store_row<BF16>(p, w.r, w.hk, w.tile * R + i / (DH / 4), (i % (DH / 4)) * 4, make_float4(0.f, 0.f, 0.f, 0.f), 0.f);
+          store_row<BF16>(p, w.r, w.hk, w.tile * R + i / (DH / 4), (i % (DH / 4)) * 4, make_float4(0.f, 0.f, 0.f, 0.f));
       if (w.at + w.len(p) >= u1) break;
       w.next(p);
       continue;
@@ -546,6 +546,13 @@ __global__ void __launch_bounds__(SplitShape<BF16, DH, NT>::THREADS, 1)
           s_l[warp][nt * 8 + 2 * t + e] = x;
         }
       }
+    // Four channels of row (nt, e) over the row's weights so far. Parts are kept and joined so, not
+    // as plain sums, which pass float32's range long before their quotient does.
+    auto mean = [&](int nt, int j, int e) {
+      const float inv = l[nt][e] == 0.f ? 0.f : 1.f / l[nt][e];
+      return make_float4(o[nt][j][e] * inv * sref, o[nt][j][e + 2] * inv * sref, o[nt][j + 1][e] * inv * sref,
+                         o[nt][j + 1][e + 2] * inv * sref);
+    };
     constexpr int CPL = DH == 64 ? 8 : 16;  // consecutive channels a lane has (of each 128)
     if constexpr (WARPS) {
       // lane (g, t): rows 2t, 2t + 1, channels g * CPL ..
@@ -560,9 +567,8 @@ __global__ void __launch_bounds__(SplitShape<BF16, DH, NT>::THREADS, 1)
 #pragma unroll
             for (int q = 0; q < CPL / 4; ++q) {
               const int ch = h * 128 + g * CPL + 4 * q;
-              const float4 a = make_float4(o[nt][h * 8 + 2 * q][e] * sref, o[nt][h * 8 + 2 * q][e + 2] * sref,
-                                           o[nt][h * 8 + 2 * q + 1][e] * sref, o[nt][h * 8 + 2 * q + 1][e + 2] * sref);
-              if (whole) store_row<BF16>(p, w.r, w.hk, w.tile * R + row, ch, a, l[nt][e]);
+              const float4 a = mean(nt, h * 8 + 2 * q, e);
+              if (whole) store_row<BF16>(p, w.r, w.hk, w.tile * R + row, ch, a);
               else *reinterpret_cast<float4*>(slot + (size_t)row * DH + ch) = a;
             }
           if (!whole && g == 0) {
@@ -583,10 +589,7 @@ __global__ void __launch_bounds__(SplitShape<BF16, DH, NT>::THREADS, 1)
             for (int h = 0; h < (DH == 256 ? 2 : 1); ++h) {
               float* d = mbuf + ((size_t)warp * RPR + row - r0) * DH + h * 128 + g * CPL;
 #pragma unroll
-              for (int q = 0; q < CPL / 4; ++q)
-                *reinterpret_cast<float4*>(d + 4 * q) =
-                    make_float4(o[nt][h * 8 + 2 * q][e] * sref, o[nt][h * 8 + 2 * q][e + 2] * sref,
-                                o[nt][h * 8 + 2 * q + 1][e] * sref, o[nt][h * 8 + 2 * q + 1][e + 2] * sref);
+              for (int q = 0; q < CPL / 4; ++q) *reinterpret_cast<float4*>(d + 4 * q) = mean(nt, h * 8 + 2 * q, e);
             }
           }
         }
@@ -596,22 +599,29 @@ __global__ void __launch_bounds__(SplitShape<BF16, DH, NT>::THREADS, 1)
         float M = -INFINITY, L = 0.f;
 #pragma unroll
         for (int k = 0; k < NCW; ++k) M = fmaxf(M, s_m[k][rr]);
+        // the warps with keys: those with weights (a warp whose scores are all NaN is one: fmaxf
+        // leaves its maximum at -inf, and its sums have to arrive)
+        float wt[NCW];
+#pragma unroll
+        for (int k = 0; k < NCW; ++k) {
+          wt[k] = s_l[k][rr];
+          if (wt[k] != 0.f) wt[k] *= ex2(s_m[k][rr] - M);
+          L += wt[k];
+        }
+        const float inv = L == 0.f ? 0.f : 1.f / L;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < NCW; ++k) {
-          const float mk = s_m[k][rr], f = mk == -INFINITY ? 0.f : ex2(mk - M);
-          // a warp without keys (not one whose scores are all NaN: fmaxf leaves its maximum at -inf
-          // too, and its sums have to arrive)
-          if (s_l[k][rr] == 0.f) continue;
+          if (wt[k] == 0.f) continue;
+          const float f = wt[k] * inv;
           const float4 x = *reinterpret_cast<const float4*>(mbuf + ((size_t)k * RPR + row) * DH + ch);
-          L += s_l[k][rr] * f;
           a.x += x.x * f;
           a.y += x.y * f;
           a.z += x.z * f;
           a.w += x.w * f;
         }
         if (whole) {
-          store_row<BF16>(p, w.r, w.hk, w.tile * R + rr, ch, a, L);
+          store_row<BF16>(p, w.r, w.hk, w.tile * R + rr, ch, a);
         } else {
           *reinterpret_cast<float4*>(slot + (size_t)rr * DH + ch) = a;
           if (ch == 0) {
@@ -650,23 +660,35 @@ __global__ void __launch_bounds__(SplitShape<BF16, DH, NT>::THREADS, 1)
         auto part_of = [&](int i) { return p.slots + (size_t)(2 * (ta + i) + (i == 0 ? 1 : 0)) * p.slot_floats; };
         for (int i = WARPS ? lane : tid; i < rows * DH / 4; i += 32 * TEAM) {
           const int rr = i / (DH / 4), ch = (i % (DH / 4)) * 4;
-          float M = -INFINITY;
-#pragma unroll 4
-          for (int k = 0; k < parts; ++k) M = fmaxf(M, __ldcg(part_of(k) + R * DH + rr));
+          float M = -INFINITY, L = 0.f;
+          for (int k0 = 0; k0 < parts; k0 += 4) {
+            float mk[4], lk[4], top = M;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float* q = part_of(min(k0 + k, parts - 1)) + R * DH + rr;
+              mk[k] = __ldcg(q);
+              lk[k] = k0 + k < parts ? __ldcg(q + R) : 0.f;
+              top = fmaxf(top, mk[k]);
+            }
+            L = L == 0.f ? 0.f : L * ex2(M - top);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) L += lk[k] == 0.f ? 0.f : lk[k] * ex2(mk[k] - top);
+            M = top;
+          }
+          const float inv = L == 0.f ? 0.f : 1.f / L;
           float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-          float L = 0.f;
 #pragma unroll 4
           for (int k = 0; k < parts; ++k) {
             const float* q = part_of(k);
-            const float mk = __ldcg(q + R * DH + rr), f = mk == -INFINITY ? 0.f : ex2(mk - M);
+            const float mk = __ldcg(q + R * DH + rr), lk = __ldcg(q + R * DH + R + rr);
             const float4 x = __ldcg(reinterpret_cast<const float4*>(q + (size_t)rr * DH + ch));
-            L += __ldcg(q + R * DH + R + rr) * f;
+            const float f = lk == 0.f ? 0.f : lk * ex2(mk - M) * inv;
             a.x += x.x * f;
             a.y += x.y * f;
             a.z += x.z * f;
             a.w += x.w * f;
           }
-          store_row<BF16>(p, w.r, w.hk, w.tile * R + rr, ch, a, L);
+          store_row<BF16>(p, w.r, w.hk, w.tile * R + rr, ch, a);
         }
       }
     }

@@ -291,17 +291,16 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Four channels of a query row (row = query * G + head in the group): sums over weights.
+// Four channels of a query row (row = query * G + head in the group).
 template <bool BF16>
-__device__ __forceinline__ void store_row(const AttnParams& p, const Req& r, int hk, int row, int ch, float4 a, float L) {
-  const float inv = L == 0.f ? 0.f : 1.f / L;
+__device__ __forceinline__ void store_row(const AttnParams& p, const Req& r, int hk, int row, int ch, float4 a) {
   const int64_t at = ((int64_t)(r.q0 + row / p.G) * p.Hq + hk * p.G + row % p.G) * p.c.dh + ch;
   if constexpr (BF16) {
-    const __nv_bfloat162 x = __floats2bfloat162_rn(a.x * inv, a.y * inv), y = __floats2bfloat162_rn(a.z * inv, a.w * inv);
+    const __nv_bfloat162 x = __floats2bfloat162_rn(a.x, a.y), y = __floats2bfloat162_rn(a.z, a.w);
     *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + at) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
   } else {
-    *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at) = make_float4(a.x, a.y, a.z, a.w);
   }
 }
 

@@ -573,7 +573,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
         tc::tc_fence_after();
         const bool whole = from == w.s.c0 && to == w.s.c1, mine = h * 128 + lrow < rows;
         float* slot = p.slots + (size_t)(2 * team + (from == w.s.c0 ? 1 : 0)) * p.slot_floats;
-        const float f = whole ? (l == 0.f ? 0.f : sref / l) : sref;
+        // over the row's weights so far, whole or part: plain sums would pass float32's range long before
+        // their quotient does (and in two factors, whose product can be too small for float32)
+        const float f = l == 0.f ? 0.f : 1.f / l;
         const int64_t at = ((int64_t)(w.r.q0 + i) * p.Hq + w.hk * p.G + row % p.G) * DH;
         uint32_t o[32];
 #pragma unroll 1
@@ -588,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
               uint32_t x[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(o[8 * q + 2 * e]) * f, __uint_as_float(o[8 * q + 2 * e + 1]) * f);
+                const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(o[8 * q + 2 * e]) * f * sref, __uint_as_float(o[8 * q + 2 * e + 1]) * f * sref);
                 x[e] = *reinterpret_cast<const uint32_t*>(&y);
               }
               d[q] = make_uint4(x[0], x[1], x[2], x[3]);
@@ -597,8 +599,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
             float4* d = reinterpret_cast<float4*>(slot + (size_t)(h * 128 + lrow) * DH + j);
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-              d[q] = make_float4(__uint_as_float(o[4 * q]) * f, __uint_as_float(o[4 * q + 1]) * f, __uint_as_float(o[4 * q + 2]) * f,
-                                 __uint_as_float(o[4 * q + 3]) * f);
+              d[q] = make_float4(__uint_as_float(o[4 * q]) * f * sref, __uint_as_float(o[4 * q + 1]) * f * sref,
+                                 __uint_as_float(o[4 * q + 2]) * f * sref, __uint_as_float(o[4 * q + 3]) * f * sref);
           }
         }
         if (!whole && mine) {
@@ -610,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
         it += max(0, to - from);  // the other half's chunks
         if (w.empty_of(u0, u1))
           for (int j = tid; j < rows * DH / 4; j += 256)
-            store_row<true>(p, w.r, w.hk, w.tile * kRows + j / (DH / 4), (j % (DH / 4)) * 4, make_float4(0.f, 0.f, 0.f, 0.f), 0.f);
+            store_row<true>(p, w.r, w.hk, w.tile * kRows + j / (DH / 4), (j % (DH / 4)) * 4, make_float4(0.f, 0.f, 0.f, 0.f));
       }
       if (from < to && !(from == w.s.c0 && to == w.s.c1)) {
         // both halves together: the last of the tile's teams joins the parts in order
@@ -632,14 +634,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
             for (int k = 0; k < parts; ++k) M = fmaxf(M, __ldcg(part_of(k) + kRows * DH + tid));
 #pragma unroll 4
             for (int k = 0; k < parts; ++k) {
-              const float mk = __ldcg(part_of(k) + kRows * DH + tid);
-              L += mk == -INFINITY ? 0.f : __ldcg(part_of(k) + kRows * DH + kRows + tid) * ex2(mk - M);
+              const float mk = __ldcg(part_of(k) + kRows * DH + tid), lk = __ldcg(part_of(k) + kRows * DH + kRows + tid);
+              L += lk == 0.f ? 0.f : lk * ex2(mk - M);
             }
             const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll 4
             for (int k = 0; k < parts; ++k) {
-              const float mk = __ldcg(part_of(k) + kRows * DH + tid);
-              __stcg(part_of(k) + kRows * DH + tid, mk == -INFINITY ? 0.f : ex2(mk - M) * inv);
+              const float mk = __ldcg(part_of(k) + kRows * DH + tid), lk = __ldcg(part_of(k) + kRows * DH + kRows + tid);
+              __stcg(part_of(k) + kRows * DH + tid, lk == 0.f ? 0.f : lk * ex2(mk - M) * inv);
             }
           }
           asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -675,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParam
 #pragma unroll
             for (int u = 0; u < U; ++u) {
               const int j = j0 + 256 * u;
-              if (j < rows * DH / 4) store_row<true>(p, w.r, w.hk, w.tile * kRows + j / (DH / 4), (j % (DH / 4)) * 4, a[u], 1.f);
+              if (j < rows * DH / 4) store_row<true>(p, w.r, w.hk, w.tile * kRows + j / (DH / 4), (j % (DH / 4)) * 4, a[u]);
             }
           }
         }

@@ -864,3 +864,18 @@ def test_attention_that_would_run_for_hours_is_refused():
         st = status_word()
         W.kv8_attention(c, q, table, dev_i32(np.array([kv])), cu_q=dev_i32(np.array([0, n])), max_q=n, out=out, status=st)
         assert int(host(st)[0]) == W.ERR_INVALID_ARG and bool((out == 7.0).all())
+
+
+@PADS
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("exponent", [119, -120])
+@pytest.mark.parametrize("kv,ql", [([300], [1]), ([9000], [130]), ([200] * 80, [1] * 79 + [30]), ([40, 500], [7, 100])])
+def test_attention_values_at_the_ends_of_float32(kv, ql, exponent, dtype, pad):
+    """Values near float32's largest and smallest numbers: results of their size, whole tiles and
+    joined parts."""
+    m, q, table, cu = attention_case(79, kv, ql, 8, 4, 128, 32, "int8", dtype, pad=pad)
+    m.v = (m.v[0], np.full(m.v[1].shape, 2.0 ** exponent))
+    m.c.v_scale.copy_(dev_f32(m.v[1]))
+    out = W.kv8_attention(m.c, q, dev_i32(table), dev_i32(np.array(kv)), cu_q=dev_i32(cu), max_q=130)
+    assert np.isfinite(f64(out)).all()
+    check_attention(out, m, q, table, kv, cu, dtype)
