@@ -368,6 +368,10 @@ __global__ void __launch_bounds__(32 * kWriteW) k_kv8_write(WriteParams p) {
       }
     }
     if (lane == 0 && (first == 0 || s != present)) *scale_at = s;
+    if (const uint32_t limit = byte_limit<E4M3>(s)) {
+      __syncwarp();
+      limit_rows<E4M3, DH>(dst, sub, RPP, first + len, limit);
+    }
   }
 }
 
@@ -487,6 +491,10 @@ __global__ void __launch_bounds__(32 * kWriteW, 3) k_kv8_write_shared(WriteParam
     }
     if (w == 0 && lane == 0 && (first == 0 || s != present)) *scale_at = s;
     if (nw > 1) __syncthreads();  // s_amax is free again
+    if (const uint32_t limit = byte_limit<E4M3>(s)) {
+      __syncwarp();
+      limit_rows<E4M3, DH>(dst, w * RPP + sub, nw * RPP, first + len, limit);
+    }
   };
 
   for (int it = blockIdx.y * kWriteW + warp; it < s_n * H2; it += gridDim.y * kWriteW)

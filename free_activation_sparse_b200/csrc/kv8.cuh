@@ -41,6 +41,37 @@ __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
   }
 }
 
+// The largest byte whose product with the scale s is finite, in all four places, where that is not
+// every byte; else 0. (A number near float32's largest rounds up to a byte that stands for 2^128:
+// 63.5 * 2^122 and above to 64 in int8, 248 * 2^120 and above to 256 in e4m3.)
+template <bool E4M3>
+__device__ __forceinline__ uint32_t byte_limit(float s) {
+  if (!(s > 0x1p119f && s < INFINITY)) return 0u;
+  const float top = __fdiv_rd(3.40282347e+38f, s);  // >= 1
+  if (top >= (E4M3 ? 448.f : 127.f)) return 0u;
+  const uint32_t b = E4M3 ? (__float_as_uint(top) >> 20) - (120u << 3) : (uint32_t)(int)top;
+  return b * 0x01010101u;
+}
+
+// Four bytes, none of a larger magnitude than byte_limit's (not 0).
+template <bool E4M3>
+__device__ __forceinline__ uint32_t limit4(uint32_t w, uint32_t limit) {
+  if constexpr (E4M3) return __vminu4(w & 0x7f7f7f7fu, limit) | (w & 0x80808080u);
+  else return __vmaxs4(__vmins4(w, limit), __vneg4(limit));
+}
+
+// Holds down (limit4) the bytes of rows i, i + step, ... below n: eight at `at` of each, DH apart.
+// Behind the stores of a page's rows rather than in them, where it would cost registers that
+// every write pays for.
+template <bool E4M3, int DH>
+__device__ __forceinline__ void limit_rows(uint8_t* at, int i, int step, int n, uint32_t limit) {
+#pragma unroll 1
+  for (; i < n; i += step) {
+    uint2* w = reinterpret_cast<uint2*>(at + i * DH);
+    *w = make_uint2(limit4<E4M3>(w->x, limit), limit4<E4M3>(w->y, limit));
+  }
+}
+
 // Four bytes to the numbers they hold (exact).
 template <bool E4M3>
 __device__ __forceinline__ void unpack4(uint32_t w, float (&f)[4]) {

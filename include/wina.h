@@ -483,7 +483,8 @@ wina_status_t kv8_plan(const int32_t* seq_len, const int32_t* new_len, int64_t B
  *   s and its present scale, and where that grows its older rows (the places before the
  *   first new one) are rounded again to the new scale;
  *   a byte is x / scale rounded to nearest even (exact up to that one rounding, since the
- *   scales are powers of two).
+ *   scales are powers of two); where that byte's product with the scale would pass float32's
+ *   range (|x| of 1.984 2^127 and above as int8, of 1.9375 2^127 as e4m3), the next one down.
  * Where a new row holds an infinity or a NaN, the page and head's scale becomes NaN and the
  * rows written are 0, so that attention over it gives NaN as it would with unquantised
  * values, until the page starts anew.

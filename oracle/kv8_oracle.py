@@ -83,6 +83,18 @@ def kv8_round(x, fmt: str):
     return np.rint(x / step) * step
 
 
+def kv8_store(x, s, fmt):
+    """What the bytes of x hold under the scale s: x / s rounded, but no further from zero than the
+    format's largest number whose product with s is a finite float32."""
+    top = float(np.finfo(np.float32).max) / s
+    if fmt == "int8":
+        top = math.floor(top)
+    elif top < 448.0:
+        m, e = math.frexp(top)  # three bits behind the leading one
+        top = math.ldexp(math.floor(m * 16.0), e - 4)
+    return np.clip(kv8_round(np.asarray(x, dtype=np.float64) / s, fmt), -top, top)
+
+
 def kv8_write(val, scale, x, slots, page, fmt):
     """val [n][H][page][dh] (the numbers the bytes hold) and scale [n][H] after the rows x
     [T][H][dh] went to `slots`; both are copies."""
@@ -108,9 +120,9 @@ def kv8_write(val, scale, x, slots, page, fmt):
             if first:
                 new = max(new, scale[p, h])
                 if new != scale[p, h]:
-                    val[p, h, :first] = kv8_round(val[p, h, :first] * (scale[p, h] / new), fmt)
+                    val[p, h, :first] = kv8_store(val[p, h, :first] * scale[p, h], new, fmt)
             scale[p, h] = new
-            val[p, h, first:first + n] = kv8_round(rows / new, fmt)
+            val[p, h, first:first + n] = kv8_store(rows, new, fmt)
         t += n
     return val, scale
 

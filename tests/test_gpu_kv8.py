@@ -879,3 +879,31 @@ def test_attention_values_at_the_ends_of_float32(kv, ql, exponent, dtype, pad):
     out = W.kv8_attention(m.c, q, dev_i32(table), dev_i32(np.array(kv)), cu_q=dev_i32(cu), max_q=130)
     assert np.isfinite(f64(out)).all()
     check_attention(out, m, q, table, kv, cu, dtype)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("page,dh", [(16, 64), (128, 256)])
+def test_write_of_finite_numbers_reads_back_finite(page, dh, dtype, fmt):
+    """Numbers around those whose byte would stand for 2^128, new and rounded again; the long run
+    goes through both write kernels' loops."""
+    t = torch()
+    m = Mirror(8, 2, page, dh, fmt)
+    rng = np.random.default_rng(4)
+    top = t.finfo(dtype_of(dtype)).max
+    edge = np.array([1.0, 0.9999, 1.984375 / 2, 1.9843 / 2, 1.9375 / 2, 1.937 / 2, 1.75 / 2, 0.5, 0.25, 2.0 ** -7, 0.0])
+    for slots, most in ((np.arange(0, page), 1.0), (page + np.arange(5), 0.4), (page + 5 + np.arange(3), 1.0),
+                        (np.array([2 * page]), 0.4961), (np.array([2 * page + 1]), 1.0), (np.array([2 * page + 2]), 0.9)):
+        x = rng.choice(edge, size=(len(slots), 2, dh)) * rng.choice([-1.0, 1.0], size=(len(slots), 2, dh)) * float(top) * most
+        x[:, :, 0] = float(top) * most
+        k = dev_f32(x.astype(np.float32)).to(dtype_of(dtype)).clamp(-top, top)
+        assert bool(t.isfinite(k).all())
+        m.write(k, k.neg(), f64(k), -f64(k), slots)
+        m.check()
+        # every place written so far (the ones behind hold a recycled page's bytes, which nobody sees)
+        seen = slots if slots[0] % page == 0 else np.arange(slots[0] // page * page, slots[-1] + 1)
+        k2, v2 = W.kv8_read(m.c, dev_i32(seen), dtype=dtype_of(dtype))
+        assert bool(t.isfinite(k2).all()) and bool(t.isfinite(v2).all())
+        if len(slots) > 1:  # half a step of the byte, or a whole one where it is held down
+            rel = ((W.kv8_read(m.c, dev_i32(slots), dtype=t.float32)[0].double() - k.double()).abs() / k.double().abs().clamp(min=1e30))[k.abs() > 0.2 * top]
+            assert float(rel.max()) <= 2.0 ** -3

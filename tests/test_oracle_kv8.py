@@ -78,3 +78,16 @@ def test_softcap_is_applied_before_the_softmax():
     out, _, _ = O.kv8_attention(q, K, V, scale=1.0, softcap=2.0)
     z = 2 * np.tanh(4.0)
     assert np.allclose(out[0, 0], [1 / (1 + np.exp(-2 * z)), 1 / (1 + np.exp(2 * z))], atol=1e-14)
+
+
+def test_what_is_stored_stands_for_a_finite_number():
+    big = float(np.finfo(np.float32).max)
+    for fmt, top in (("int8", 63.0 * 2.0 ** 122), ("e4m3", 240.0 * 2.0 ** 120)):
+        val, scale = np.zeros((1, 1, 16, 1)), np.zeros((1, 1))
+        val, scale = O.kv8_write(val, scale, np.array([[[big]], [[-big]], [[top]]]), [0, 1, 2], 16, fmt)
+        assert (val[0, 0, :3, 0] * scale[0, 0]).tolist() == [top, -top, top]
+    # older rows that are rounded again: 127 * 2^121 is a tie between 63 and 64 times 2^122
+    val, scale = O.kv8_write(np.zeros((1, 1, 16, 1)), np.zeros((1, 1)), np.array([[[127.0 * 2.0 ** 121]]]), [0], 16, "int8")
+    assert scale[0, 0] == 2.0 ** 121 and val[0, 0, 0, 0] == 127.0
+    val, scale = O.kv8_write(val, scale, np.array([[[big]]]), [1], 16, "int8")
+    assert scale[0, 0] == 2.0 ** 122 and val[0, 0, :2, 0].tolist() == [63.0, 63.0]
