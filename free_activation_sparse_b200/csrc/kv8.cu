@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(kReadT) k_kv8_read(ReadParams p) {
 
 static int page_shift(int64_t page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
 
-static bool page_ok(int64_t page) { return page == 16 || page == 32 || page == 64 || page == 128; }
+static bool page_ok(int64_t page) { return page == 16 || page == 32 || page == 64 || page == kMaxPage; }
 
 wina_status_t kv8_cache_check(const kv8_cache_t* c) {
   if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale) return WINA_ERR_INVALID_ARG;
@@ -637,7 +637,9 @@ extern "C" wina_status_t kv8_plan(const int32_t* seq_len, const int32_t* new_len
 template <bool BF16, bool E4M3, int DH>
 static void (*write_kernel(int64_t page))(WriteParams) {
   constexpr int ROWS = (BF16 ? 8 : 4) * (32 / (DH / 8));  // rows that a warp holds
-  return page > 4 * ROWS ? k_kv8_write_shared<BF16, E4M3, DH> : k_kv8_write<BF16, E4M3, DH>;
+  if constexpr (kMaxPage > 4 * ROWS)  // (bf16 rows of 64: no page is that long)
+    if (page > 4 * ROWS) return k_kv8_write_shared<BF16, E4M3, DH>;
+  return k_kv8_write<BF16, E4M3, DH>;
 }
 
 template <bool BF16, bool E4M3>

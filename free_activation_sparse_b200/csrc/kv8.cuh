@@ -13,6 +13,7 @@ namespace wina {
 namespace kv8 {
 
 constexpr int kMaxB = 8192;                  // requests of one call, at most
+constexpr int kMaxPage = 128;                // places of a page, at most
 constexpr int kScaleEMin = -120, kScaleEMax = 122;
 
 // The smallest power of two s with amax <= qmax * s, from the bits of a finite amax >= 0:

@@ -5,11 +5,14 @@ raise."""
 from __future__ import annotations
 
 import ctypes
+import shutil
+import subprocess
 
 import pytest
 import torch
 
 import free_activation_sparse_b200 as W
+from free_activation_sparse_b200 import build
 
 FAKE = 1 << 20  # a 16-byte-aligned address that is never dereferenced
 ODD = FAKE + 2
@@ -154,3 +157,19 @@ def test_binding_raises_on_bad_tensors():
         W.Kv8Cache(c.k, c.v[:2], c.k_scale, c.v_scale)._struct()
     with pytest.raises(ValueError):
         W.Kv8Cache(c.k, c.v, c.k_scale[:2], c.v_scale)._struct()
+
+
+def test_no_write_kernel_is_built_that_no_call_reaches():
+    """kv8_write shares a run among warps where a page is more than four times the rows of 8 (bf16)
+    or 4 (float32) passes of a warp, and pages have 128 places at most: not for bf16 rows of 64."""
+    nm = shutil.which("nm")
+    if nm is None:
+        pytest.skip("no nm")
+    names = subprocess.run([nm, "-C", build.LIB], capture_output=True, text=True, check=True).stdout
+    for bf16 in (True, False):
+        for e4m3 in ("true", "false"):
+            for dh in (64, 128, 256):
+                rows = (8 if bf16 else 4) * (32 // (dh // 8))
+                name = f"k_kv8_write_shared<{str(bf16).lower()}, {e4m3}, {dh}>"
+                assert (name in names) == (128 > 4 * rows), name
+                assert name.replace("_shared", "") in names
