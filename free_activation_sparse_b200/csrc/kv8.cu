@@ -188,6 +188,7 @@ __global__ void __launch_bounds__(kPlanT) k_kv8_plan(PlanParams p) {
       const bool ok = pg[i] >= 0 && pg[i] <= (0x7fffffff >> p.shift);
       sl[i] = ok ? (pg[i] << p.shift) | (ps[i] & (page - 1)) : -1;
       if (!ok) ps[i] = 0;
+      if (!ok && at[i]) record_status(p.status, WINA_ERR_INVALID_ARG);  // a table or stack entry that is no page
     }
     if (t0 + 4 <= p.tokens) {
       *reinterpret_cast<int4*>(p.slots + t0) = make_int4(sl[0], sl[1], sl[2], sl[3]);

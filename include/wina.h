@@ -456,7 +456,9 @@ typedef struct {
  *   kv_len: device int32 [B]: the lengths with the new tokens (may be seq_len itself).
  *   cu_q: device int32 [B + 1]: exclusive prefix sums of the new tokens (at most `tokens`).
  *   slots: device int32 [tokens]: every new token's slot, in the order of requests; -1 for
- *     the places behind the last token (a padded batch) and for tokens without a page.
+ *     the places behind the last token (a padded batch) and for tokens without a page. A page
+ *     index that is negative, or whose slots would pass 31 bits, is no page (kv8_plan does not
+ *     know n_pages): WINA_ERR_INVALID_ARG.
  *   positions: optional device int32 [tokens]: every new token's position in its request
  *     (0 where slots is -1).
  *   n_free_out: device int32 [1]: the pages free afterwards (may be n_free itself).

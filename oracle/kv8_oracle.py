@@ -60,6 +60,8 @@ def kv8_plan(seq_len, new_len, table, free_pages, n_free, page, tokens):
             if 0 <= p <= (2 ** 31 - 1) // page:
                 slots[at + i] = p * page + (s + i) % page
                 pos[at + i] = s + i
+            else:
+                bad = True
     a = lambda v: np.array(v, dtype=np.int64)  # noqa: E731
     return dict(kv_len=a(kv), cu_q=np.minimum(a(cu), tokens), slots=a(slots), positions=a(pos), n_free=left, table=table,
                 free_pages=cells, short=short, bad=bad)

@@ -907,3 +907,29 @@ def test_write_of_finite_numbers_reads_back_finite(page, dh, dtype, fmt):
         if len(slots) > 1:  # half a step of the byte, or a whole one where it is held down
             rel = ((W.kv8_read(m.c, dev_i32(slots), dtype=t.float32)[0].double() - k.double()).abs() / k.double().abs().clamp(min=1e30))[k.abs() > 0.2 * top]
             assert float(rel.max()) <= 2.0 ** -3
+
+
+def test_plan_reports_entries_that_are_no_pages():
+    """On the stack and in a request's table: the tokens get no slot, and the status says why."""
+    seq, new, table = np.array([5, 20, 0, 3]), np.array([1, 30, 4, 0]), np.full((4, 4), -1)
+    table[0, 0], table[1, :2], table[3, 0] = 3, (1, 2), -9  # request 3 brings no token: nobody looks
+    cells = np.array([6, 5, 4, 7, -1])
+    assert not check_plan(seq, new, table, cells, 4, 16, 40)["bad"]
+    for wrong in (-1, -2 ** 31, 2 ** 27, 2 ** 31 - 1):
+        for at in (2, 3):  # popped by request 2 and by request 1
+            c2 = cells.copy()
+            c2[at] = wrong
+            want = check_plan(seq, new, table, c2, 4, 16, 40)
+            assert want["bad"] and (want["slots"][:35] < 0).any() and (want["slots"][:35] >= 0).any()
+        t2 = table.copy()
+        t2[1, 1] = wrong
+        assert check_plan(seq, new, t2, cells, 4, 16, 40)["bad"]
+    # one wrong entry past 4096 tokens, where a cluster shares the plan
+    rng = np.random.default_rng(6)
+    seq, new, table, cells, n_free, tokens = plan_case(rng, 60, 16, 40, 300, 4, 5)
+    assert tokens > 4096 and not check_plan(seq, new, table, cells, n_free, 16, tokens)["bad"]
+    pushed = int((-(-seq // 16))[new < 0].sum())  # popped first
+    need = int((-(-(seq + np.maximum(new, 0)) // 16) + -seq // 16)[new >= 0].sum())
+    assert need > pushed + 50
+    cells[n_free - 1 - (need - pushed) // 2] = -1
+    assert check_plan(seq, new, table, cells, n_free, 16, tokens)["bad"]
