@@ -92,8 +92,9 @@ struct SplitShape {
 //                 not mind;
 //   running max, p = 2^(s - max + 14), sum p in float32;
 //   O^T += V^T P^T with P = p vs / sref in float16 (float32: two parts), sref the largest
-//                 value scale met so far: a weight keeps 11 (22) bits down to 2^-28 of the
-//                 largest, and O is rescaled where max or sref grow.
+//                 value scale met so far: P keeps 11 bits down to 2^-28 of the row's largest weight
+//                 (22 down to 2^-16) and is within 2^-39 of it below; O is rescaled where max or
+//                 sref grow.
 // The matrix instruction's additions to its accumulator do not round to nearest, so for float32
 // queries a chunk's sums are made apart and added in float32, and the second parts' scores apart
 // from the first's (2-norm errors at 9 K keys: 0.4e-6 to 0.9e-6, and 0.7e-6 to 3.2e-6 without, for

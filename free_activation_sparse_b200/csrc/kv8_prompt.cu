@@ -142,8 +142,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // tensor cores work for the other.
 //   warps 8-15 (bytes): a chunk's keys and values from the pages into shared memory as float16
 //     times 8 scale / reference, the reference being the first chunk's largest scale, raised
-//     when a scale passes 16 times it: exact for power-of-two scales over 2^17 of range, so a
-//     score needs one factor per row and chunk and a weight none. Loads run a chunk ahead.
+//     when a scale passes 16 times it, so a score needs one factor per row and chunk and a weight
+//     none. Exact for power-of-two scales down to 2^-27 (int8; e4m3, whose numbers start at 2^-9:
+//     2^-18) of the reference: 8 * 2^-27 is float16's least number. Loads run a chunk ahead.
 //   warp 16: S = Q K^T of either half as soon as its last P has been used, O += P V as soon as P
 //     is there (P is the A operand from tensor memory, in the place of S).
 //   warps 0-3, 4-7 (softmax, a thread per row): the row's maximum in one pass over S, the

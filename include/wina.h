@@ -529,9 +529,19 @@ wina_status_t kv8_read(const kv8_cache_t* cache, const int32_t* slots, int64_t T
  *   nothing and records WINA_ERR_INVALID_ARG. 1 <= B <= 8192, Hq / Hkv <= 64, T <= 2^24. out overlaps neither q
  *   nor the pages. A wait inside the kernel is bounded (1 s; WINA_ERR_TIMEOUT).
  *   Deterministic: fixed-order sums throughout, so the same call gives the same bits.
- *   bf16: the weights are rounded to float16 with their value scales (11 bits down to 2^-19
- *   of a row's largest), the queries and bytes are exact; float32: queries and weights are
- *   held as two float16 parts (22 bits). e4m3 bytes are numbers (kv8_write stores no NaN). */
+ *   What is rounded besides (a tile is 8 to 256 query rows of one request and key/value head):
+ *     queries: float16 times a power of two per row, exact for bf16 down to 2^-28 of the row's
+ *       largest element; float32 as two such parts (22 bits).
+ *     Short rows and float32: a weight, times its page's value scale over the largest value
+ *       scale of the pages its tile has read, to float16: 11 bits (float32: two parts, 22), but
+ *       to no less than 2^-39 of the row's largest weight. Bytes are exact.
+ *     Prompt chunks of bf16 (more than 96 query rows for each request and head, dh 64 and 128): a
+ *       weight to float16 (11 bits down to 2^-21 of the row's largest), a byte times its scale
+ *       over the largest scale of its tile's pages so far to float16, which is exact while that
+ *       quotient is a power of two of at least 2^-18 (e4m3) or 2^-27 (int8).
+ *     A tile's pages are those that any of its rows sees: a page that is louder than the others by
+ *     more than this leaves room for also costs digits in rows of the tile that do not see it.
+ *   e4m3 bytes are numbers (kv8_write stores no NaN). */
 wina_status_t kv8_attention(const kv8_cache_t* cache, const void* q, wina_dtype_t qdt, int64_t T, int64_t ld_q,
                             int64_t Hq, const int32_t* table, int64_t width, const int32_t* kv_len,
                             const int32_t* cu_q, int64_t B, int64_t max_q, float scale, int64_t window, float softcap,

@@ -735,6 +735,10 @@ def test_attention_tiles_that_see_no_key(kv, n, B, hq, hkv, dh, pad, dtype):
         assert not f64(out)[cu[b]:cu[b + 1] - kv].any(), b
     check_attention(out, m, q, table, [kv] * B, cu, dtype)
     assert (f64(out)[cu[-1]:] == 7.0).all()
+    W.kv8_attention(m.c, q, dev_i32(table), dev_i32(np.array([kv] * B)), ws=ws, out=out.fill_(7.0), softcap=5.0, **args)
+    for b in range(B):
+        assert not f64(out)[cu[b]:cu[b + 1] - kv].any(), b
+    check_attention(out, m, q, table, [kv] * B, cu, dtype, softcap=5.0)
     assert not ws.buf[:160 * 12 * 4].any()  # the teams' arrival counters, which lead the workspace
     m2, q2, table2, cu2 = attention_case(n, [3000] * B, [min(n, 200)] * B, hq, hkv, dh, 16, "int8", dtype, pad=pad)
     args = dict(cu_q=dev_i32(cu2), max_q=n)
@@ -933,3 +937,53 @@ def test_plan_reports_entries_that_are_no_pages():
     assert need > pushed + 50
     cells[n_free - 1 - (need - pushed) // 2] = -1
     assert check_plan(seq, new, table, cells, n_free, 16, tokens)["bad"]
+
+
+@pytest.mark.parametrize("fmt,apart", [("int8", 27), ("e4m3", 18)])
+@pytest.mark.parametrize("side", ["k", "v"])
+@pytest.mark.parametrize("at", [1, 3])
+def test_attention_prompt_tile_with_a_page_louder_by_the_stated_range(at, side, fmt, apart):
+    """The tensor-core kernel holds a tile's bytes against its loudest page. Up to the stated quotient
+    that is exact: rows that see quiet pages only (those before page `at`, in one tile with rows
+    that see it) are as without it, and values of every row are within the usual bounds."""
+    kv, n, page = 200, 200, 16
+    m, q, table, cu = attention_case(80 + at, [kv], [n], 8, 2, 128, page, fmt, "bf16", pad=5200)
+    args = (dev_i32(table), dev_i32(np.array([kv])))
+    more = dict(cu_q=dev_i32(cu), max_q=n)
+    assert at * page < 256 // 4  # the tile of the first 64 queries
+    (val, scale), dev = (m.k, m.c.k_scale) if side == "k" else (m.v, m.c.v_scale)
+    scale = np.full(scale.shape, 2.0 ** -6)
+    scale[table[0, at]] = 2.0 ** (apart - 6)
+    dev.copy_(dev_f32(scale))
+    if side == "k":
+        m.k = (val, scale)
+    else:
+        m.v = (val, scale)
+    out = W.kv8_attention(m.c, q, *args, **more)
+    rows_ = at * page
+    check_attention(out[:rows_], m, q[:rows_], table, [rows_], [0, rows_], "bf16")
+    if side == "v":
+        check_attention(out, m, q, table, [kv], cu, "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dh", [64, 128, 256])
+def test_attention_short_tile_with_a_page_far_louder(dh, dtype):
+    """The kernel of short rows: weights are within 2^-39 of the row's largest, times the loud
+    page's scale over a quiet one's, in rows that do not see it as well."""
+    kv, n, page, apart = 40, 12, 32, 18
+    m, q, table, cu = attention_case(90, [kv], [n], 1, 1, dh, page, "int8", dtype)
+    scale = np.full(m.v[1].shape, 2.0 ** -6)
+    scale[table[0, 1]] = 2.0 ** (apart - 6)
+    m.v = (m.v[0], scale)
+    m.c.v_scale.copy_(dev_f32(scale))
+    half, weight = (2.0 ** -8, 2.0 ** -11) if dtype == "bf16" else (2.0 ** -24, 2.0 ** -22)
+    for length, loud in ((kv, 2.0 ** apart), (page, 1.0)):  # of 40 keys, the first 4 queries see 32 at most
+        out = f64(W.kv8_attention(m.c, q, dev_i32(table), dev_i32(np.array([length])), cu_q=dev_i32(cu), max_q=n))
+        K, V = cached(m, table, 0, length)
+        want, mass, size = O.kv8_attention(f64(q), K, V)
+        es = size[:, :, None] * (dh + 8) * 2.0 ** -23
+        tol = half * np.abs(want) + mass * (weight + np.expm1(2 * es) + 2.0 ** -21 + length * 2.0 ** -23)
+        # 2^-39 of the largest weight, for each key that the row sees
+        tol += 2.0 ** -39 * loud * np.stack([np.abs(V[:length - n + i + 1]).sum(0) for i in range(n)])
+        assert (np.abs(out - want) <= tol).all(), length
