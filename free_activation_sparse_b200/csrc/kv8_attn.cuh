@@ -266,7 +266,8 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // The four bytes of w as float16 numbers, two to a word. Exact: int8 through 1024 + (byte + 128),
-// whose float16 step is 1 (the word already xor-ed by biased()); e4m3 is a subset of float16.
+// whose float16 step is 1, the long published way to put a byte into a mantissa (the word
+// already xor-ed by biased()); e4m3 is a subset of float16.
 template <bool E4M3>
 __device__ __forceinline__ void half4_of(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if constexpr (E4M3) {

@@ -149,7 +149,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 //     is there (P is the A operand from tensor memory, in the place of S).
 //   warps 0-3, 4-7 (softmax, a thread per row): the row's maximum in one pass over S, the
 //     weights as float16 in a second; O is rescaled only when a maximum outgrows its
-//     reference by 2^8 (a weight keeps 11 bits from 2^15 down to 2^-14).
+//     reference by 2^8, a published idea (a weight keeps 11 bits from 2^15 down to 2^-14).
 // Queries are float16 times a power of two per row (exact for bf16 within 2^28 of the row's
 // largest). Places without a page or outside the tile's keys are zeros. A half whose bytes of a
 // page are no numbers (kv8_write stores none) may get NaN where it does not see them.
@@ -160,7 +160,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // weights 2.5 K; with the conversions, the exponentials and the first pass left out together it
 // still takes 0.70 ms. Slower: four softmax warps a quarter (1.02 ms, spills), S by 64 keys in
 // two places a half (1.00 ms, twice the hand-overs), both passes unrolled (1.23 ms, instruction
-// caches), four warps for the bytes (1.74 ms).
+// caches; with four warps for the bytes and no packed arithmetic besides, 1.74 ms: four such
+// warps were not tried with the short loops).
 template <bool E4M3, int DH>
 __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_prompt(const AttnParams p) {
   using Sh = PromptShape<DH>;

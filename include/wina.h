@@ -488,8 +488,8 @@ wina_status_t kv8_plan(const int32_t* seq_len, const int32_t* new_len, int64_t B
  *   scales are powers of two); where that byte's product with the scale would pass float32's
  *   range (|x| of 1.984 2^127 and above as int8, of 1.9375 2^127 as e4m3), the next one down.
  * Where a new row holds an infinity or a NaN, the page and head's scale becomes NaN and the
- * rows written are 0, so that attention over it gives NaN as it would with unquantised
- * values, until the page starts anew.
+ * rows written are 0, so that attention gives NaN, as it would with unquantised values, to
+ * every row that sees a key of that page (its older keys included), until the page starts anew.
  *   k, v: device [T][heads][dh] of xdt with ld_k, ld_v elements from one token's row to
  *     the next (slices of a fused projection's output); 16-byte aligned, ld * size a
  *     multiple of 16 bytes, ld >= heads * dh.
