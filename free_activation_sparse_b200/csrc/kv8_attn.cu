@@ -101,8 +101,9 @@ struct SplitShape {
 // 2 % of the time, or 15 % with 16 rows).
 // The bytes' conversion and the softmax, some 420 instructions a chunk of 32 keys in one
 // dependent stream, are what a warp spends its time on; twelve warps hide its latency (64 long
-// contexts, 1.3 GB: 207 us, 6.3 TB/s; 264 us with eight warps).
-// A team's warps' (max, sum, O / sum) are joined in shared memory in warp order; a tile cut by a
+// contexts, 1.3 GB: 208 us, 6.3 TB/s; 264 us with eight warps).
+// A team's warps' (max, sum, O / sum) are joined in shared memory in warp order (their sums tell
+// which warps have keys; a warp of NaN scores has no maximum but a sum); a tile cut by a
 // part's end is left in the workspace, and the last team of that tile to arrive joins the
 // parts in order. No team waits for another.
 template <bool BF16, bool E4M3, int DH, int NT, bool WARPS>

@@ -155,7 +155,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // page are no numbers (kv8_write stores none) may get NaN where it does not see them.
 //
 // 4 chunks of up to 2048 queries behind 2 K to 6 K keys (32 / 8 heads of 128, 0.52 TFLOP): 0.80 ms,
-// 654 TFLOP/s; a step of 128 keys takes 5.4 K cycles, of which the tensor cores work 2.1 K. What
+// 650 TFLOP/s; a step of 128 keys takes 5.4 K cycles, of which the tensor cores work 2.1 K. What
 // holds it is the chain of a half: products 1.6 K cycles with their hand-overs, maxima 0.9 K,
 // weights 2.5 K; with the conversions, the exponentials and the first pass left out together it
 // still takes 0.70 ms. Slower: four softmax warps a quarter (1.02 ms, spills), S by 64 keys in
