@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(32 * kWriteW) k_kv8_write(WriteParams p) {
     if (lane == 0 && (first == 0 || s != present)) *scale_at = s;
     if (const uint32_t limit = byte_limit<E4M3>(s)) {
       __syncwarp();
-      limit_rows<E4M3, DH>(dst, sub, RPP, first + len, limit);
+      limit_rows<E4M3, DH>(dst, (s == present ? first : 0) + sub, RPP, first + len, limit);
     }
   }
 }
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(32 * kWriteW, 3) k_kv8_write_shared(WriteParam
     if (nw > 1) __syncthreads();  // s_amax is free again
     if (const uint32_t limit = byte_limit<E4M3>(s)) {
       __syncwarp();
-      limit_rows<E4M3, DH>(dst, w * RPP + sub, nw * RPP, first + len, limit);
+      limit_rows<E4M3, DH>(dst, (s == present ? first : 0) + w * RPP + sub, nw * RPP, first + len, limit);
     }
   };
 

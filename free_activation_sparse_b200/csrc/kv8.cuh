@@ -62,8 +62,8 @@ __device__ __forceinline__ uint32_t limit4(uint32_t w, uint32_t limit) {
 }
 
 // Holds down (limit4) the bytes of rows i, i + step, ... below n: eight at `at` of each, DH apart.
-// Behind the stores of a page's rows rather than in them, where it would cost registers that
-// every write pays for.
+// Behind the stores of a page's rows (the new ones, and the older ones that were rounded again)
+// rather than in them, where it would cost registers that every write pays for.
 template <bool E4M3, int DH>
 __device__ __forceinline__ void limit_rows(uint8_t* at, int i, int step, int n, uint32_t limit) {
 #pragma unroll 1

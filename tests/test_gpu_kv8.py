@@ -987,3 +987,20 @@ def test_attention_short_tile_with_a_page_far_louder(dh, dtype):
         # 2^-39 of the largest weight, for each key that the row sees
         tol += 2.0 ** -39 * loud * np.stack([np.abs(V[:length - n + i + 1]).sum(0) for i in range(n)])
         assert (np.abs(out - want) <= tol).all(), length
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("page,dh", [(16, 128), (128, 64), (128, 256)])
+def test_write_leaves_older_rows_whose_scale_stays(page, dh, fmt):
+    """Also under the largest scales, and bytes that no write of this library would leave there."""
+    rng = np.random.default_rng(5)
+    m = Mirror(4, 2, page, dh, fmt)
+    big = np.full(m.k[1].shape, 2.0 ** 122)
+    m.k, m.v = (m.k[0], big), (m.v[0], big)
+    m.c.k_scale.copy_(dev_f32(big))
+    m.c.v_scale.copy_(dev_f32(big))
+    for slots in (np.arange(3, page), page + np.array([page - 1]), 2 * page + np.arange(2, 12)):
+        for dtype in ("f32", "bf16"):
+            k, kf = rows(rng, (len(slots), 2, dh), dtype)
+            m.write(k, k, kf, kf, slots)
+            m.check()
